@@ -30,9 +30,12 @@ EXPORTED = (
     "kin_sparse_decode_attn_paged", "kin_block_means_build_ex", "kin_block_means_update_ex",
     "kin_block_topk_select_ex", "kin_token_topk_workspace_bytes", "kin_token_topk_decode_attn",
     "kin_block_topk_select_paged", "kin_dual_means_bytes", "kin_dual_page_means_bytes",
+    "kin_kv4_store", "kin_kv4_append", "kin_kv4_load", "kin_kv_attn_workspace_bytes", "kin_kv_decode_attn",
+    "kin_kv_evict_workspace_bytes", "kin_kv_evict",
 )
 KIN_MEANS_F32, KIN_MEANS_BF16, KIN_MEANS_DUAL = 0, 1, 2
 KIN_MEANS_PER_PAGE = 0x100
+KIN_KV_BF16, KIN_KV_INT4 = 0, 1
 NOALLOC_SCRATCH_FLOATS = 1 << 21  # KIN_NOALLOC_SCRATCH_FLOATS in include/kin.h
 
 
@@ -54,6 +57,18 @@ class kin_dims(ctypes.Structure):
 
     def __repr__(self):
         return "kin_dims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class kin_kv(ctypes.Structure):
+    _fields_ = [
+        ("format", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("block_table", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+    ]
 
 
 def make_dims(batch, num_kv_heads, num_q_heads, head_dim, block_size, max_seq_len) -> kin_dims:
@@ -113,6 +128,21 @@ def load_library(path: str = LIB_PATH):
     lib.kin_dual_means_bytes.restype = sz
     lib.kin_dual_page_means_bytes.argtypes = [dp, i32]
     lib.kin_dual_page_means_bytes.restype = sz
+    kp = ctypes.POINTER(kin_kv)
+    lib.kin_kv4_store.argtypes = [dp, kp, kp, vp, vp, i32, vp, vp]
+    lib.kin_kv4_store.restype = ctypes.c_int
+    lib.kin_kv4_append.argtypes = [dp, kp, vp, i32, vp, vp, vp, vp, i32, vp, vp]
+    lib.kin_kv4_append.restype = ctypes.c_int
+    lib.kin_kv4_load.argtypes = [dp, kp, vp, vp, i32, vp, vp, vp, vp]
+    lib.kin_kv4_load.restype = ctypes.c_int
+    lib.kin_kv_attn_workspace_bytes.argtypes = [dp, i32, i32]
+    lib.kin_kv_attn_workspace_bytes.restype = sz
+    lib.kin_kv_decode_attn.argtypes = [dp, vp, kp, vp, vp, vp, i32, f32, vp, vp, vp, vp, sz, vp, vp]
+    lib.kin_kv_decode_attn.restype = ctypes.c_int
+    lib.kin_kv_evict_workspace_bytes.argtypes = [dp, i32]
+    lib.kin_kv_evict_workspace_bytes.restype = sz
+    lib.kin_kv_evict.argtypes = [dp, kp, vp, vp, i32, i32, i32, dp, kp, vp, vp, vp, i32, vp, vp, sz, vp, vp]
+    lib.kin_kv_evict.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -463,3 +493,167 @@ def kin_block_topk_select_paged(dims, q, page_means, block_table, seq_lens, k_bl
         _dev(sel_cnt, "sel_cnt", torch.int32, count=c.pairs), _dev(workspace, "workspace"),
         workspace.numel() * workspace.element_size(), _status(dev_status), _stream(stream))
     _check(rc, "kin_block_topk_select_paged")
+
+
+# ------------------------------------- 4-bit caches, attention weights, eviction
+
+class KvCache:
+    """A KV cache as the kin_kv_* calls take it: bf16 rows (no scales), or
+    4-bit codes (uint8) with their bf16 scales; contiguous, or a page pool
+    with its block_table.  Holds the tensors it is made of."""
+
+    __slots__ = ("k", "v", "k_scales", "v_scales", "block_table")
+
+    def __init__(self, k, v, k_scales=None, v_scales=None, block_table=None):
+        if (k_scales is None) != (v_scales is None):
+            raise ValueError("a 4-bit cache has k_scales and v_scales")
+        self.k, self.v, self.k_scales, self.v_scales, self.block_table = k, v, k_scales, v_scales, block_table
+
+    @property
+    def int4(self) -> bool:
+        return self.k_scales is not None
+
+    def _struct(self, c: "_Counts", name: str):
+        """The C descriptor, after the checks every call makes of its tensors."""
+        pages, table, elements = 0, None, c.cache
+        if self.block_table is not None:
+            pages = int(self.k.shape[0])
+            table = _dev(self.block_table, name + ".block_table", torch.int32, count=c.table)
+            elements = c.times(pages, c.page)
+        codes = None if elements is None else elements // 2
+        rows = (torch.uint8, codes) if self.int4 else (_BF16, elements)
+        kv = kin_kv(KIN_KV_INT4 if self.int4 else KIN_KV_BF16, pages, table,
+                    _dev(self.k, name + ".k", rows[0], count=rows[1]), _dev(self.v, name + ".v", rows[0], count=rows[1]))
+        if self.int4:
+            scales = None if elements is None else elements // 32
+            kv.k_scales = _dev(self.k_scales, name + ".k_scales", _BF16, count=scales)
+            kv.v_scales = _dev(self.v_scales, name + ".v_scales", _BF16, count=scales)
+        return kv, pages
+
+
+def alloc_kv4(dims: kin_dims, num_pages: Optional[int] = None, block_table=None, device="cuda") -> KvCache:
+    """A zero-filled 4-bit cache for these dims: contiguous, or a pool of
+    num_pages pages found through block_table."""
+    if (num_pages is None) != (block_table is None):
+        raise ValueError("a page pool needs num_pages and block_table")
+    if num_pages is None:
+        shape = (dims.batch, dims.num_kv_heads, dims.max_seq_len)
+    else:
+        shape = (int(num_pages), dims.num_kv_heads, dims.block_size)
+    codes = [torch.zeros(shape + (dims.head_dim // 2,), dtype=torch.uint8, device=device) for _ in range(2)]
+    scales = [torch.zeros(shape + (dims.head_dim // 32,), dtype=torch.bfloat16, device=device) for _ in range(2)]
+    return KvCache(*codes, *scales, block_table=block_table)
+
+
+def _kv_means(block_means, c: _Counts, dims, pages, per_page):
+    """The optional block means beside a cache: pointer and dtype code."""
+    if block_means is None:
+        return None, KIN_MEANS_F32
+    means, dtype = _means(block_means, c.times(pages, c.page_mean) if per_page else c.means, dims=dims,
+                          pages=pages if per_page else None)
+    return means, dtype | (KIN_MEANS_PER_PAGE if per_page else 0)
+
+
+def kin_kv4_store(dims, src: KvCache, dst: KvCache, seq_lens, block_means=None, dev_status=None, stream=None,
+                  per_page=False):
+    """A prefilled bf16 cache into a 4-bit one, with its block means."""
+    c = _Counts(dims)
+    s, _ = src._struct(c, "src")
+    d, pages = dst._struct(c, "dst")
+    means, dtype = _kv_means(block_means, c, dims, pages, per_page)
+    rc = load_library().kin_kv4_store(
+        ctypes.byref(dims), ctypes.byref(s), ctypes.byref(d), _dev(seq_lens, "seq_lens", torch.int32, count=c.lens),
+        means, dtype, _status(dev_status), _stream(stream))
+    _check(rc, "kin_kv4_store")
+
+
+def kin_kv4_append(dims, kv: KvCache, block_means, seq_lens, new_lens, k_new, v_new, n_new, dev_status=None,
+                   stream=None, per_page=False):
+    """n_new tokens onto a 4-bit cache; new_lens may be seq_lens (in place)."""
+    c = _Counts(dims)
+    d, pages = kv._struct(c, "kv")
+    means, dtype = _kv_means(block_means, c, dims, pages, per_page)
+    new_rows = c.times(max(int(n_new), 0), c.bkd)
+    rc = load_library().kin_kv4_append(
+        ctypes.byref(dims), ctypes.byref(d), means, dtype, _dev(seq_lens, "seq_lens", torch.int32, count=c.lens),
+        _dev(new_lens, "new_lens", torch.int32, count=c.lens), _dev(k_new, "k_new", _BF16, count=new_rows),
+        _dev(v_new, "v_new", _BF16, count=new_rows), int(n_new), _status(dev_status), _stream(stream))
+    _check(rc, "kin_kv4_append")
+
+
+def kin_kv4_load(dims, kv: KvCache, seq_lens, k_out, v_out, starts=None, n=None, dev_status=None, stream=None):
+    """Rows of a 4-bit cache as bf16: n tokens a sequence from starts (0 when
+    not given) into k_out / v_out [B, Hkv, n, D]; n defaults to k_out's."""
+    c = _Counts(dims)
+    d, _ = kv._struct(c, "kv")
+    n = int(k_out.shape[2]) if n is None else int(n)
+    rows = c.times(max(n, 0), c.bkd)
+    rc = load_library().kin_kv4_load(
+        ctypes.byref(dims), ctypes.byref(d), _dev(seq_lens, "seq_lens", torch.int32, count=c.lens),
+        _dev(starts, "starts", torch.int32, nullable=True, count=c.lens), n, _dev(k_out, "k_out", _BF16, count=rows),
+        _dev(v_out, "v_out", _BF16, count=rows), _status(dev_status), _stream(stream))
+    _check(rc, "kin_kv4_load")
+
+
+def kin_kv_attn_workspace_bytes(dims: kin_dims, k_blocks: int, with_acc: bool = False) -> int:
+    return int(load_library().kin_kv_attn_workspace_bytes(ctypes.byref(dims), int(k_blocks), int(with_acc)))
+
+
+def alloc_kv_attn_workspace(dims: kin_dims, k_blocks: int, acc: bool = False, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace of kin_kv_attn_workspace_bytes."""
+    n = kin_kv_attn_workspace_bytes(dims, k_blocks, acc)
+    if n == 0:
+        raise KinError(1, "kin_kv_attn_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def kin_kv_decode_attn(dims, q, kv: KvCache, seq_lens, sel_idx, sel_cnt, k_blocks, softmax_scale, out, lse, workspace,
+                       acc=None, dev_status=None, stream=None):
+    """Decode attention over a bf16 or 4-bit cache; sel_idx and sel_cnt None
+    with k_blocks 0 attend to every block; acc [B, Hkv, Lcap] fp32 takes the
+    attention weights on top of what it holds."""
+    c = _Counts(dims)
+    d, _ = kv._struct(c, "kv")
+    k = int(k_blocks)
+    acc_rows = None if c.cache is None else c.cache // dims.head_dim
+    rc = load_library().kin_kv_decode_attn(
+        ctypes.byref(dims), _dev(q, "q", _BF16, count=c.q), ctypes.byref(d),
+        _dev(seq_lens, "seq_lens", torch.int32, count=c.lens),
+        _dev(sel_idx, "sel_idx", torch.int32, nullable=True, count=c.times(max(k, 0), c.pairs)),
+        _dev(sel_cnt, "sel_cnt", torch.int32, nullable=True, count=c.pairs), k, float(softmax_scale),
+        _dev(out, "out", _BF16, count=c.q), _dev(lse, "lse", torch.float32, nullable=True, count=c.lse),
+        _dev(acc, "acc", torch.float32, nullable=True, count=acc_rows), _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _status(dev_status), _stream(stream))
+    _check(rc, "kin_kv_decode_attn")
+
+
+def kin_kv_evict_workspace_bytes(dims: kin_dims, n_keep: int) -> int:
+    return int(load_library().kin_kv_evict_workspace_bytes(ctypes.byref(dims), int(n_keep)))
+
+
+def alloc_kv_evict_workspace(dims: kin_dims, n_keep: int, device="cuda") -> torch.Tensor:
+    n = kin_kv_evict_workspace_bytes(dims, n_keep)
+    if n == 0:
+        raise KinError(1, "kin_kv_evict_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def kin_kv_evict(dims, kv: KvCache, acc, seq_lens, n_keep, n_sink, n_recent, dst_dims, dst: KvCache, dst_acc, dst_lens,
+                 workspace, block_means=None, sel_tokens=None, dev_status=None, stream=None, per_page=False):
+    """The n_keep tokens of every (sequence, KV head) that stay (first n_sink,
+    last n_recent, then by acc), moved in order to the cache dst."""
+    c, cd = _Counts(dims), _Counts(dst_dims)
+    s, _ = kv._struct(c, "kv")
+    d, pages = dst._struct(cd, "dst")
+    means, dtype = _kv_means(block_means, cd, dst_dims, pages, per_page)
+    rows = None if c.cache is None else c.cache // dims.head_dim
+    dst_rows = None if cd.cache is None else cd.cache // dst_dims.head_dim
+    rc = load_library().kin_kv_evict(
+        ctypes.byref(dims), ctypes.byref(s), _dev(acc, "acc", torch.float32, count=rows),
+        _dev(seq_lens, "seq_lens", torch.int32, count=c.lens), int(n_keep), int(n_sink), int(n_recent),
+        ctypes.byref(dst_dims), ctypes.byref(d), _dev(dst_acc, "dst_acc", torch.float32, nullable=True, count=dst_rows),
+        _dev(dst_lens, "dst_lens", torch.int32, count=c.lens), means, dtype,
+        _dev(sel_tokens, "sel_tokens", torch.int32, nullable=True, count=c.times(max(int(n_keep), 0), c.pairs)),
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _status(dev_status),
+        _stream(stream))
+    _check(rc, "kin_kv_evict")

@@ -111,6 +111,7 @@ kin_status check_dims(const kin_dims* d) {
 }
 
 constexpr int kMaxDevices = 64;
+constexpr int kSmemSlots = 24;
 
 int device_sm_count() {
   // per device, written once with the same value by whichever thread gets there first
@@ -132,13 +133,14 @@ cudaError_t ensure_smem_limit(const void* kernel, int slot, size_t bytes) {
   // device) never exceeds the limit in force.
   // slots in use: 0, 2, 3, then 8, 9, 10, then 12, 13, 14 block top-k (256,
   // 512, 1024 threads; plain, refining, refining per page), 1 attention, 4
-  // means update, 5 token top-k, 6 token logits
-  static std::atomic<size_t> done[16][kMaxDevices];
+  // means update, 5 token top-k, 6 token logits, 7 eviction select, 16..19
+  // attention over a cache of either format
+  static std::atomic<size_t> done[kSmemSlots][kMaxDevices];
   static std::mutex mu;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const bool cached = dev >= 0 && dev < kMaxDevices && slot >= 0 && slot < 16;
+  const bool cached = dev >= 0 && dev < kMaxDevices && slot >= 0 && slot < kSmemSlots;
   if (cached && done[slot][dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
   std::lock_guard<std::mutex> lock(mu);
   cudaFuncAttributes attr;
@@ -603,5 +605,303 @@ KIN_EXPORT kin_status kin_token_topk_decode_attn(const kin_dims* dims, const voi
   cudaError_t e = launch_token_logits(p, s);
   if (e == cudaSuccess) e = launch_token_topk(p, s);
   if (e == cudaSuccess) e = launch_token_attn(p, s);
+  return from_cuda(e);
+}
+
+// ------------------------------------------------- KV caches of either format
+namespace {
+
+// A cache descriptor against dims: format, pointers, pages.
+kin_status kv_view(const kin_dims& d, const kin_kv* kv, KvView* out) {
+  if (!kv || (kv->format != KIN_KV_BF16 && kv->format != KIN_KV_INT4)) return KIN_ERR_INVALID_ARG;
+  const bool int4 = kv->format == KIN_KV_INT4;
+  if (!kv->k || !kv->v || !aligned16(kv->k) || !aligned16(kv->v)) return KIN_ERR_INVALID_ARG;
+  if (int4 && (!kv->k_scales || !kv->v_scales || !aligned16(kv->k_scales) || !aligned16(kv->v_scales)))
+    return KIN_ERR_INVALID_ARG;
+  *out = KvView{};
+  out->pages = contiguous();
+  if (kv->block_table) {
+    kin_status st = check_pages(d, kv->k, kv->num_pages, kv->block_table, &out->pages);
+    if (st != KIN_OK) return st;
+  }
+  out->k = static_cast<uint8_t*>(kv->k);
+  out->v = static_cast<uint8_t*>(kv->v);
+  out->ks = int4 ? static_cast<uint16_t*>(kv->k_scales) : nullptr;
+  out->vs = int4 ? static_cast<uint16_t*>(kv->v_scales) : nullptr;
+  out->int4 = int4;
+  out->Lcap = d.max_seq_len;
+  return KIN_OK;
+}
+
+// Optional block means written beside a cache: their layout, and the row
+// stride of the dual form.
+kin_status means_layout(const kin_dims& d, const KvView& kv, const void* means, int32_t dtype, int* flag, int* per_page,
+                        int64_t* rows) {
+  *flag = means_flag(dtype);
+  *per_page = per_page_flag(dtype);
+  *rows = 0;
+  if (!means) return KIN_OK;
+  if (*flag < 0 || !aligned16(means)) return KIN_ERR_INVALID_ARG;
+  if (*per_page && !kv.pages.table) return KIN_ERR_INVALID_ARG;
+  *rows = *per_page ? (int64_t)kv.pages.num_pages * d.num_kv_heads : (int64_t)pairs_of(d) * nbcap_of(d);
+  return KIN_OK;
+}
+
+// The two share a buffer, a page pool included.
+bool same_cache(const KvView& a, const KvView& b) { return a.k == b.k || a.v == b.v || a.k == b.v || a.v == b.k; }
+
+#ifndef KIN_KV4_CHUNK_TOKENS
+#define KIN_KV4_CHUNK_TOKENS 768
+#endif
+
+// Kept blocks per attention CTA: 768 tokens (110 KB of 4-bit rows), fewer
+// when the grid would hold fewer than 2 CTAs per SM.
+int kv_chunk_blocks(const kin_dims& d, int k) {
+  const int by_tokens = KIN_KV4_CHUNK_TOKENS / d.block_size > 0 ? KIN_KV4_CHUNK_TOKENS / d.block_size : 1;
+  const int64_t by_grid = (int64_t)k * pairs_of(d) / (2 * kTargetSMs);
+  int ch = by_tokens;
+  if (by_grid < ch) ch = by_grid > 0 ? (int)by_grid : 1;
+  const int cap = kMaxItemTiles / (d.block_size / kTileTokens);
+  return ch < cap ? ch : cap;
+}
+
+// The slots of the kept blocks of a pair: at most k_blocks, at most all.
+int kv_slots(const kin_dims& d, int k_blocks) {
+  const int nb = nbcap_of(d);
+  return k_blocks == 0 || k_blocks > nb ? nb : k_blocks;
+}
+
+struct KvWs {
+  size_t counters, partials, z, lse2, total;
+};
+
+// The select's regions first (its counters' place is this call's too), so
+// that one buffer serves both.
+KvWs kv_ws_layout(const kin_dims& d, int k_blocks, bool acc) {
+  KvWs w;
+  const size_t pairs = (size_t)pairs_of(d), g = (size_t)(d.num_q_heads / d.num_kv_heads);
+  const int k = kv_slots(d, k_blocks);
+  size_t off = 0;
+  w.counters = 0;
+  off = k_blocks >= 2 ? ws_layout(d, k_blocks).total : align_up(pairs * sizeof(uint32_t));
+  w.partials = off;
+  const int ch = kv_chunk_blocks(d, k);
+  off = align_up(off + pairs * (size_t)((k + ch - 1) / ch) * g * kPartStride * sizeof(float));
+  w.z = off;
+  if (acc) off = align_up(off + pairs * (size_t)k * d.block_size * g * sizeof(float));
+  w.lse2 = off;
+  if (acc) off = align_up(off + pairs * g * sizeof(float));
+  w.total = off;
+  return w;
+}
+
+}  // namespace
+
+KIN_EXPORT kin_status kin_kv4_store(const kin_dims* dims, const kin_kv* src, const kin_kv* dst,
+                                    const int32_t* seq_lens, void* block_means, int32_t means_dtype,
+                                    int32_t* dev_status, void* stream) {
+  KIN_NVTX_RANGE();
+  kin_status st = check_dims(dims);
+  if (st != KIN_OK) return st;
+  KvView s, d;
+  if ((st = kv_view(*dims, src, &s)) != KIN_OK || (st = kv_view(*dims, dst, &d)) != KIN_OK) return st;
+  if (s.int4 || !d.int4 || !seq_lens) return KIN_ERR_INVALID_ARG;
+  Kv4WriteParams p{};
+  st = means_layout(*dims, d, block_means, means_dtype, &p.means_flag, &p.means_per_page, &p.mean_rows);
+  if (st != KIN_OK) return st;
+  p.dst = d;
+  p.k_src = s.k;
+  p.v_src = s.v;
+  p.src_pages = s.pages;
+  p.seq_lens = seq_lens;
+  p.means = block_means;
+  p.dev_status = dev_status;
+  p.B = dims->batch;
+  p.Hkv = dims->num_kv_heads;
+  p.bs = dims->block_size;
+  p.nbcap = nbcap_of(*dims);
+  p.span = p.nbcap;
+  return from_cuda(launch_kv4_write(p, static_cast<cudaStream_t>(stream)));
+}
+
+KIN_EXPORT kin_status kin_kv4_append(const kin_dims* dims, const kin_kv* kv, void* block_means, int32_t means_dtype,
+                                     const int32_t* seq_lens, int32_t* new_lens, const void* k_new, const void* v_new,
+                                     int32_t n_new, int32_t* dev_status, void* stream) {
+  KIN_NVTX_RANGE();
+  kin_status st = check_dims(dims);
+  if (st != KIN_OK) return st;
+  if ((st = check_update_count(dims, n_new)) != KIN_OK) return st;
+  KvView d;
+  if ((st = kv_view(*dims, kv, &d)) != KIN_OK) return st;
+  if (!d.int4 || !seq_lens || !new_lens || !k_new || !v_new) return KIN_ERR_INVALID_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new)) return KIN_ERR_INVALID_ARG;
+  Kv4WriteParams p{};
+  st = means_layout(*dims, d, block_means, means_dtype, &p.means_flag, &p.means_per_page, &p.mean_rows);
+  if (st != KIN_OK) return st;
+  if (n_new == 0 && new_lens == seq_lens) return KIN_OK;
+  p.dst = d;
+  p.k_src = static_cast<const uint8_t*>(k_new);
+  p.v_src = static_cast<const uint8_t*>(v_new);
+  p.src_pages = contiguous();
+  p.seq_lens = seq_lens;
+  p.new_lens = new_lens;
+  p.means = n_new ? block_means : nullptr;
+  p.dev_status = dev_status;
+  p.append = 1;
+  p.B = dims->batch;
+  p.Hkv = dims->num_kv_heads;
+  p.bs = dims->block_size;
+  p.nbcap = nbcap_of(*dims);
+  p.n_new = n_new;
+  p.span = n_new ? (n_new + p.bs - 2) / p.bs + 1 : 1;  // blocks that n_new rows can touch
+  return from_cuda(launch_kv4_write(p, static_cast<cudaStream_t>(stream)));
+}
+
+KIN_EXPORT kin_status kin_kv4_load(const kin_dims* dims, const kin_kv* kv, const int32_t* seq_lens,
+                                   const int32_t* starts, int32_t n, void* k_out, void* v_out, int32_t* dev_status,
+                                   void* stream) {
+  KIN_NVTX_RANGE();
+  kin_status st = check_dims(dims);
+  if (st != KIN_OK) return st;
+  if (n < 0) return KIN_ERR_INVALID_ARG;
+  if (n > dims->max_seq_len) return KIN_ERR_CAPACITY;
+  KvView s;
+  if ((st = kv_view(*dims, kv, &s)) != KIN_OK) return st;
+  if (!s.int4 || !seq_lens || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return KIN_ERR_INVALID_ARG;
+  if (n == 0) return KIN_OK;
+  Kv4LoadParams p{};
+  p.src = s;
+  p.seq_lens = seq_lens;
+  p.starts = starts;
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.v_out = static_cast<__nv_bfloat16*>(v_out);
+  p.dev_status = dev_status;
+  p.B = dims->batch;
+  p.Hkv = dims->num_kv_heads;
+  p.bs = dims->block_size;
+  p.n = n;
+  return from_cuda(launch_kv4_load(p, static_cast<cudaStream_t>(stream)));
+}
+
+KIN_EXPORT size_t kin_kv_attn_workspace_bytes(const kin_dims* dims, int32_t k_blocks, int32_t with_acc) {
+  if (check_dims(dims) != KIN_OK || k_blocks < 0 || k_blocks == 1) return 0;
+  return kv_ws_layout(*dims, k_blocks, with_acc != 0).total;
+}
+
+KIN_EXPORT kin_status kin_kv_decode_attn(const kin_dims* dims, const void* q, const kin_kv* kv, const int32_t* seq_lens,
+                                         const int32_t* sel_idx, const int32_t* sel_cnt, int32_t k_blocks,
+                                         float softmax_scale, void* out, float* lse, float* acc, void* workspace,
+                                         size_t ws_bytes, int32_t* dev_status, void* stream) {
+  KIN_NVTX_RANGE();
+  kin_status st = check_dims(dims);
+  if (st != KIN_OK) return st;
+  // no selection: every block (k_blocks 0); else both arrays and a budget
+  if (k_blocks < 0 || k_blocks == 1 || (k_blocks == 0) != (sel_idx == nullptr) || (k_blocks == 0) != (sel_cnt == nullptr))
+    return KIN_ERR_INVALID_ARG;
+  KvAttnParams p{};
+  if ((st = kv_view(*dims, kv, &p.kv)) != KIN_OK) return st;
+  if (!q || !seq_lens || !out || !aligned16(q) || !aligned16(out)) return KIN_ERR_INVALID_ARG;
+  if (!(softmax_scale == softmax_scale) || std::isinf(softmax_scale)) return KIN_ERR_INVALID_ARG;
+  const KvWs w = kv_ws_layout(*dims, k_blocks, acc != nullptr);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0 || ws_bytes < w.total)
+    return KIN_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.seq_lens = seq_lens;
+  p.sel_idx = sel_idx;
+  p.sel_cnt = sel_cnt;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.lse2 = reinterpret_cast<float*>(ws + w.lse2);
+  p.z = reinterpret_cast<float*>(ws + w.z);
+  p.acc = acc;
+  p.partials = reinterpret_cast<float*>(ws + w.partials);
+  p.counters = reinterpret_cast<uint32_t*>(ws + w.counters);
+  p.dev_status = dev_status;
+  p.B = dims->batch;
+  p.Hkv = dims->num_kv_heads;
+  p.Hq = dims->num_q_heads;
+  p.g = dims->num_q_heads / dims->num_kv_heads;
+  p.bs = dims->block_size;
+  p.k_row = k_blocks;
+  p.k = kv_slots(*dims, k_blocks);
+  p.chunk_blocks = kv_chunk_blocks(*dims, p.k);
+  p.max_chunks = (p.k + p.chunk_blocks - 1) / p.chunk_blocks;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)kHeadDim);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  return from_cuda(launch_kv_attn(p, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+struct EvictWs {
+  size_t sel, keys, total;
+};
+
+EvictWs evict_ws_layout(const kin_dims& d, int n_keep) {
+  EvictWs w;
+  const size_t pairs = (size_t)pairs_of(d);
+  size_t off = 0;
+  w.sel = off;
+  off = align_up(off + pairs * (size_t)n_keep * sizeof(int32_t));
+  w.keys = off;
+  if (d.max_seq_len > kTokenKeyCap) off = align_up(off + pairs * (size_t)d.max_seq_len * sizeof(uint32_t));
+  w.total = off;
+  return w;
+}
+
+}  // namespace
+
+KIN_EXPORT size_t kin_kv_evict_workspace_bytes(const kin_dims* dims, int32_t n_keep) {
+  if (check_dims(dims) != KIN_OK || n_keep < 1 || n_keep > dims->max_seq_len) return 0;
+  return evict_ws_layout(*dims, n_keep).total;
+}
+
+KIN_EXPORT kin_status kin_kv_evict(const kin_dims* dims, const kin_kv* kv, const float* acc, const int32_t* seq_lens,
+                                   int32_t n_keep, int32_t n_sink, int32_t n_recent, const kin_dims* dst_dims,
+                                   const kin_kv* dst, float* dst_acc, int32_t* dst_lens, void* block_means,
+                                   int32_t means_dtype, int32_t* sel_tokens, void* workspace, size_t ws_bytes,
+                                   int32_t* dev_status, void* stream) {
+  KIN_NVTX_RANGE();
+  kin_status st = check_dims(dims);
+  if (st != KIN_OK || (st = check_dims(dst_dims)) != KIN_OK) return st;
+  if (n_keep < 1 || n_sink < 0 || n_recent < 0 || (int64_t)n_sink + n_recent > n_keep) return KIN_ERR_INVALID_ARG;
+  if (n_keep > dims->max_seq_len || n_keep > dst_dims->max_seq_len) return KIN_ERR_CAPACITY;
+  if (dst_dims->batch != dims->batch || dst_dims->num_kv_heads != dims->num_kv_heads ||
+      dst_dims->num_q_heads != dims->num_q_heads || dst_dims->block_size != dims->block_size)
+    return KIN_ERR_INVALID_ARG;
+  EvictParams p{};
+  if ((st = kv_view(*dims, kv, &p.src)) != KIN_OK || (st = kv_view(*dst_dims, dst, &p.dst)) != KIN_OK) return st;
+  if (p.src.int4 != p.dst.int4 || !acc || !seq_lens || !dst_lens) return KIN_ERR_INVALID_ARG;
+  // every head's tokens move at once: the two caches are two buffers, or
+  // disjoint pages of one pool
+  if (same_cache(p.src, p.dst) && !(p.src.pages.table && p.dst.pages.table && p.src.k == p.dst.k && p.src.v == p.dst.v))
+    return KIN_ERR_INVALID_ARG;
+  if (p.src.pages.table && p.src.pages.table == p.dst.pages.table && p.src.k == p.dst.k) return KIN_ERR_INVALID_ARG;
+  if (dst_acc == acc || dst_lens == seq_lens) return KIN_ERR_INVALID_ARG;
+  st = means_layout(*dst_dims, p.dst, block_means, means_dtype, &p.means_flag, &p.means_per_page, &p.mean_rows);
+  if (st != KIN_OK) return st;
+  const EvictWs w = evict_ws_layout(*dims, n_keep);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0 || ws_bytes < w.total)
+    return KIN_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.acc = acc;
+  p.dst_acc = dst_acc;
+  p.seq_lens = seq_lens;
+  p.dst_lens = dst_lens;
+  p.sel = sel_tokens ? sel_tokens : reinterpret_cast<int32_t*>(ws + w.sel);
+  p.key_scratch = reinterpret_cast<uint32_t*>(ws + w.keys);
+  p.means = block_means;
+  p.dev_status = dev_status;
+  p.B = dims->batch;
+  p.Hkv = dims->num_kv_heads;
+  p.bs = dims->block_size;
+  p.nbcap_dst = nbcap_of(*dst_dims);
+  p.n_keep = n_keep;
+  p.n_sink = n_sink;
+  p.n_recent = n_recent;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_evict_select(p, s);
+  if (e == cudaSuccess) e = launch_evict_move(p, s);
   return from_cuda(e);
 }

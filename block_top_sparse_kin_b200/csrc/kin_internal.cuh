@@ -322,6 +322,100 @@ struct TokenParams {
   float scale;                   // softmax scale (natural log base)
 };
 
+// ------------------------------------------------- KV caches of either format
+// A cache as kin_kv describes it.  INT4 rows: kCodeBytes bytes of codes and
+// kGroups bf16 scales, one per kGroupDim channels (see kin.h).
+constexpr int kGroupDim = 32;
+constexpr int kGroups = kHeadDim / kGroupDim;
+constexpr int kCodeBytes = kHeadDim / 2;
+
+struct KvView {
+  uint8_t* k;   // bf16 rows, or codes
+  uint8_t* v;
+  uint16_t* ks;  // scales [rows][kGroups] (INT4)
+  uint16_t* vs;
+  PageTable pages;
+  int int4;
+  int Lcap;
+};
+
+// Row index of token t of pair (b, h) in a cache, or -1 when its page index
+// lies outside the pool.
+__device__ __forceinline__ int64_t kv_row(const PageTable& pt, int b, int h, int Hkv, int Lcap, int bs, int t) {
+  if (!pt.table) return ((int64_t)b * Hkv + h) * Lcap + t;
+  const int i = t / bs;
+  const int page = __ldg(pt.table + (int64_t)b * pt.max_blocks + i);
+  if (page < 0 || page >= pt.num_pages) return -1;
+  return ((int64_t)page * Hkv + h) * bs + (t - i * bs);
+}
+
+// Store (first = 0, rows from a bf16 cache) and append (rows from k_new /
+// v_new behind the first seq_lens[b] tokens) into a 4-bit cache.
+struct Kv4WriteParams {
+  KvView dst;
+  const uint8_t* k_src;  // bf16 rows: a cache (store) or [B][Hkv][n_new][D] (append)
+  const uint8_t* v_src;
+  PageTable src_pages;   // store only
+  const int32_t* seq_lens;
+  int32_t* new_lens;     // append only
+  void* means;           // may be null
+  int means_flag;        // 0 fp32, 1 bf16, 2 dual
+  int64_t mean_rows;
+  int means_per_page;
+  int32_t* dev_status;
+  int append;
+  int B, Hkv, bs, nbcap, n_new;
+  int span;              // blocks a (b, h) may touch
+};
+
+struct Kv4LoadParams {
+  KvView src;
+  const int32_t* seq_lens;
+  const int32_t* starts;  // may be null: 0
+  __nv_bfloat16* k_out;   // [B][Hkv][n][D]
+  __nv_bfloat16* v_out;
+  int32_t* dev_status;
+  int B, Hkv, bs, n;
+};
+
+// Decode attention over a cache of either format; acc: accumulated weights.
+struct KvAttnParams {
+  const __nv_bfloat16* q;
+  KvView kv;
+  const int32_t* seq_lens;
+  const int32_t* sel_idx;  // null: every block
+  const int32_t* sel_cnt;
+  __nv_bfloat16* out;
+  float* lse;              // may be null
+  float* lse2;             // workspace [B][Hq], base 2 (acc only)
+  float* z;                // workspace [pairs][k][bs][g] base-2 logits (acc only)
+  float* acc;              // [B][Hkv][Lcap], may be null
+  float* partials;
+  uint32_t* counters;
+  int32_t* dev_status;
+  int B, Hkv, Hq, g, bs;
+  int k, k_row;            // kept blocks a pair may have; stride of sel_idx
+  int chunk_blocks, max_chunks;
+  float scale_log2;
+};
+
+// Eviction: the kept tokens of every pair, then their move.
+struct EvictParams {
+  KvView src, dst;
+  const float* acc;        // [B][Hkv][src Lcap]
+  float* dst_acc;          // [B][Hkv][dst Lcap], may be null
+  const int32_t* seq_lens;
+  int32_t* dst_lens;
+  int32_t* sel;            // [pairs][n_keep]
+  uint32_t* key_scratch;   // [pairs][src Lcap] when it exceeds the shared-memory key cap
+  void* means;             // may be null
+  int means_flag;
+  int64_t mean_rows;
+  int means_per_page;
+  int32_t* dev_status;
+  int B, Hkv, bs, nbcap_dst, n_keep, n_sink, n_recent;
+};
+
 // Launch with programmatic stream serialization (see pdl_wait).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
@@ -358,5 +452,10 @@ cudaError_t launch_attn(const AttnParams& p, int num_items, cudaStream_t s);
 cudaError_t launch_token_logits(const TokenParams& p, cudaStream_t s);
 cudaError_t launch_token_topk(const TokenParams& p, cudaStream_t s);
 cudaError_t launch_token_attn(const TokenParams& p, cudaStream_t s);
+cudaError_t launch_kv4_write(const Kv4WriteParams& p, cudaStream_t s);
+cudaError_t launch_kv4_load(const Kv4LoadParams& p, cudaStream_t s);
+cudaError_t launch_kv_attn(const KvAttnParams& p, cudaStream_t s);
+cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s);
+cudaError_t launch_evict_move(const EvictParams& p, cudaStream_t s);
 
 }  // namespace kin

@@ -730,7 +730,12 @@ __device__ __forceinline__ void select_from_keys(const uint32_t* keys, uint8_t* 
 // smallest and largest candidate key, and zeroes both histograms.  With both
 // rows 16-byte aligned, whole groups of 4 scores move as 16-byte loads and
 // stores, 8 per thread in flight; the rest one score at a time.
-template <int NT>
+// KeyOf maps a score's bits to its key.
+struct ScoreKey {
+  static __device__ __forceinline__ uint32_t of(uint32_t u) { return key_of_bits(u); }
+};
+
+template <int NT, typename KeyOf = ScoreKey>
 __device__ __forceinline__ void load_keys(const uint32_t* sc, uint32_t* keys, int nb, const Cands& cd, TopkSmem<NT>& sm,
                                           uint32_t& kmin, uint32_t& kmax) {
   constexpr int NW = NT / 32;
@@ -753,7 +758,7 @@ __device__ __forceinline__ void load_keys(const uint32_t* sc, uint32_t* keys, in
       for (int u = 0; u < kVec; ++u) {
         const int j = base + u * NT + tid;
         if (j < nv) {
-          const uint4 kk = make_uint4(key_of_bits(v[u].x), key_of_bits(v[u].y), key_of_bits(v[u].z), key_of_bits(v[u].w));
+          const uint4 kk = make_uint4(KeyOf::of(v[u].x), KeyOf::of(v[u].y), KeyOf::of(v[u].z), KeyOf::of(v[u].w));
           keys4[j] = kk;
           const int i = 4 * j;
           if (i >= cd.lo && i + 3 <= cd.hi) {
@@ -782,7 +787,7 @@ __device__ __forceinline__ void load_keys(const uint32_t* sc, uint32_t* keys, in
     for (int u = 0; u < kBatch; ++u) {
       const int i = base + u * NT + tid;
       if (i < nb) {
-        const uint32_t key = key_of_bits(v[u]);
+        const uint32_t key = KeyOf::of(v[u]);
         keys[i] = key;
         if (cd.has(i)) {
           lo = min(lo, key);
@@ -813,7 +818,7 @@ __device__ __forceinline__ void load_keys(const uint32_t* sc, uint32_t* keys, in
 // memory when nb <= key_cap (skey holds key_cap words, then key_cap bytes
 // for the keys' bins), else gkeys (nb words of global scratch, which may be
 // the score row itself when nothing reads it afterwards).
-template <int NT>
+template <int NT, typename KeyOf = ScoreKey>
 __device__ __forceinline__ void topk_memory(const uint32_t* row, int nb, const Cands& cd, int k, int32_t* sel,
                                             uint32_t* skey, int key_cap, uint32_t* gkeys, TopkSmem<NT>& sm,
                                             int32_t* dev_status) {
@@ -821,7 +826,7 @@ __device__ __forceinline__ void topk_memory(const uint32_t* row, int nb, const C
   uint32_t* keys = in_smem ? skey : gkeys;
   uint8_t* bins = in_smem ? reinterpret_cast<uint8_t*>(skey + key_cap) : nullptr;
   uint32_t kmin, kmax;
-  load_keys(row, keys, nb, cd, sm, kmin, kmax);
+  load_keys<NT, KeyOf>(row, keys, nb, cd, sm, kmin, kmax);
   select_from_keys(keys, bins, nb, cd, k, kmin, kmax, sel, sm, dev_status);
 }
 
@@ -986,14 +991,14 @@ __device__ __forceinline__ void topk_regs_keys(const uint32_t (&key)[KPT], int n
 
 // The top-k of one pair with nb <= KPT * NT blocks, keys held in registers:
 // thread t loads blocks u * NT + t (u < KPT) from the score row.
-template <int NT, int KPT>
+template <int NT, int KPT, typename KeyOf = ScoreKey>
 __device__ __forceinline__ void topk_regs(const uint32_t* row, int nb, const Cands& cd, int k, int32_t* sel, uint32_t* skey,
                                           TopkSmem<NT>& sm, int32_t* dev_status) {
   uint32_t key[KPT];
 #pragma unroll
   for (int u = 0; u < KPT; ++u) {
     const int i = u * NT + threadIdx.x;
-    key[u] = i < nb ? key_of_bits(__ldcg(row + i)) : 0u;
+    key[u] = i < nb ? KeyOf::of(__ldcg(row + i)) : 0u;
   }
   topk_regs_keys<NT, KPT>(key, nb, cd, k, sel, skey, sm, dev_status);
 }
@@ -1980,6 +1985,61 @@ cudaError_t launch_token_topk(const TokenParams& p, cudaStream_t s) {
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(token_topk_kernel), 5, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(token_topk_kernel, dim3(p.B * p.Hq), dim3(kTokTopkThreads), smem, s, p);
+}
+
+// ---- eviction: which tokens of a pair stay.  Key of an accumulated weight:
+// its value (-0 as +0), NaN below everything.
+struct WeightKey {
+  static __device__ __forceinline__ uint32_t of(uint32_t u) {
+    const float f = __uint_as_float(u);
+    return f != f ? 0u : float_key(f + 0.0f);
+  }
+};
+
+// One 1024-thread CTA per (sequence, KV head): the first n_sink and the last
+// n_recent tokens are forced, the rest of the n_keep slots go to the largest
+// weights (ties to the lower index), ascending; every token when the budget
+// covers the length.  The threshold search is the token top-k's, over the
+// candidate range [n_sink, L - n_recent).  The first head's CTA writes the
+// sequence's new length.
+__global__ void __launch_bounds__(kTokTopkThreads, 1) evict_select_kernel(EvictParams p) {
+  extern __shared__ uint32_t skey[];  // as token_topk_kernel's
+  __shared__ TopkSmem<kTokTopkThreads> sm;
+  const int tid = threadIdx.x;
+  pdl_wait();
+  pdl_trigger_early();
+  const int64_t pair = blockIdx.x;
+  const int b = (int)(pair / p.Hkv);
+  const int h = (int)(pair - (int64_t)b * p.Hkv);
+  const int Lcap = p.src.Lcap, k = p.n_keep;
+  int32_t* sel = p.sel + pair * k;
+  int L = __ldg(p.seq_lens + b);
+  if (L < 0 || L > Lcap) {  // nothing kept
+    if (tid == 0) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
+    L = 0;
+  }
+  if (h == 0 && tid == 0) p.dst_lens[b] = min(L, k);
+  if (L <= k) {
+    for (int i = tid; i < k; i += kTokTopkThreads) sel[i] = i < L ? i : -1;
+    return;
+  }
+  const uint32_t* row = reinterpret_cast<const uint32_t*>(p.acc + pair * Lcap);
+  const Cands cd{p.n_sink, L - p.n_recent - 1, k - p.n_sink - p.n_recent};
+  if (L <= 4 * kTokTopkThreads)
+    topk_regs<kTokTopkThreads, 4, WeightKey>(row, L, cd, k, sel, skey, sm, p.dev_status);
+  else if (L <= 8 * kTokTopkThreads)
+    topk_regs<kTokTopkThreads, 8, WeightKey>(row, L, cd, k, sel, skey, sm, p.dev_status);
+  else
+    topk_memory<kTokTopkThreads, WeightKey>(row, L, cd, k, sel, skey, min(Lcap, kTokKeyCap),
+                                            p.key_scratch + pair * Lcap, sm, p.dev_status);
+}
+
+cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s) {
+  const size_t cap = (size_t)(p.src.Lcap < kTokKeyCap ? p.src.Lcap : kTokKeyCap);
+  const size_t smem = cap * sizeof(uint32_t) + ((cap + 3) & ~size_t(3));  // keys, then their bins
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(evict_select_kernel), 7, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(evict_select_kernel, dim3(p.B * p.Hkv), dim3(kTokTopkThreads), smem, s, p);
 }
 
 // Threads per top-k CTA: enough for 4 keys per thread (up to 4096 blocks),

@@ -328,6 +328,118 @@ kin_status kin_block_topk_select_noalloc(const kin_dims* dims, const void* q, co
                                          const int32_t* seq_lens, int32_t k_blocks, int32_t* sel_idx,
                                          int32_t* sel_cnt, int32_t* dev_status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * KV caches in 4 bits, accumulated attention weights, eviction.
+ *
+ * A long generation outgrows its cache: these calls hold the rows in 4 bits
+ * (144 bytes a token and KV head instead of 512), and keep only the tokens
+ * that attention has weighed most.  They take a cache as a kin_kv:
+ *   format       KIN_KV_BF16: k and v are the bf16 rows of the calls above.
+ *                KIN_KV_INT4: k and v are codes, 64 bytes a row, and k_scales
+ *                and v_scales 4 bf16 a row, each tensor laid out like the
+ *                bf16 rows ([B][Hkv][Lcap][64] and [B][Hkv][Lcap][4], or
+ *                pages [num_pages][Hkv][bs][64] and [num_pages][Hkv][bs][4]).
+ *   block_table  NULL: contiguous (num_pages ignored); else as in the paged
+ *                calls.
+ *
+ * A 4-bit row.  Each group of 32 channels holds
+ *   a = max |x|,  s = bf16(a / 7),  c = clamp(round(x / s), -7, 7)
+ * (rounded half to even; c = 0 where s = 0) and stands for c s.  A group
+ * that holds NaN or an infinity has s = NaN and c = 0 and stands for NaN.
+ * A code is the nibble c + 8, low nibble first.  Key rows: word 4c + g (c and
+ * g 0..3; little endian) holds channels 32g + 8c + e, even e in nibbles 0..3,
+ * odd e in nibbles 4..7.  Value rows: halfword 4r + g (r 0..7) holds channels
+ * 32g + 4r .. 32g + 4r + 3.  scale g is that of channels 32g .. 32g + 31.
+ *
+ * Block means beside a 4-bit cache are those of the values held (fp32 sums in
+ * token order, divided by the count), in any means_dtype of the extended
+ * calls, KIN_MEANS_PER_PAGE included; block_means NULL leaves them out.  The
+ * select calls read them unchanged. */
+typedef enum { KIN_KV_BF16 = 0, KIN_KV_INT4 = 1 } kin_kv_format;
+typedef struct {
+  int32_t format;             /* kin_kv_format */
+  int32_t num_pages;          /* with a block_table */
+  const int32_t* block_table; /* [B][ceil(Lcap / bs)] or NULL */
+  void* k;
+  void* v;
+  void* k_scales;             /* KIN_KV_INT4 only */
+  void* v_scales;
+} kin_kv;
+
+/* Stores the first seq_lens[b] tokens of every sequence of a bf16 cache src
+ * in the 4-bit cache dst (the two may have different block tables), and the
+ * means of their blocks.  Rows and blocks behind the length are left as they
+ * were.  A length outside [0, Lcap], or a page index outside its pool, skips
+ * that sequence or block and flags KIN_ERR_DEVICE_DATA. */
+kin_status kin_kv4_store(const kin_dims* dims, const kin_kv* src, const kin_kv* dst, const int32_t* seq_lens,
+                         void* block_means, int32_t means_dtype, int32_t* dev_status, void* stream);
+
+/* Appends n_new tokens to every sequence of a 4-bit cache: k_new / v_new
+ * ([B][Hkv][n_new][D] bf16) go to rows seq_lens[b] + r, the means of the
+ * blocks that hold one of them are taken again from all their rows, and
+ * new_lens[b] = seq_lens[b] + n_new.  new_lens may be seq_lens itself (in
+ * place; a second small launch then).  A length below 0 or with no room for
+ * n_new is skipped, keeps its length and flags KIN_ERR_DEVICE_DATA.  An
+ * append and a store of the same tokens leave the same bytes. */
+kin_status kin_kv4_append(const kin_dims* dims, const kin_kv* kv, void* block_means, int32_t means_dtype,
+                          const int32_t* seq_lens, int32_t* new_lens, const void* k_new, const void* v_new,
+                          int32_t n_new, int32_t* dev_status, void* stream);
+
+/* Reads rows starts[b] .. starts[b] + n - 1 of a 4-bit cache back as bf16
+ * (each value rounded to nearest even) into k_out / v_out [B][Hkv][n][D].
+ * starts NULL begins at 0; rows at or behind seq_lens[b] come back as zeros,
+ * so do those of a bad length, start or page (flagged). */
+kin_status kin_kv4_load(const kin_dims* dims, const kin_kv* kv, const int32_t* seq_lens, const int32_t* starts,
+                        int32_t n, void* k_out, void* v_out, int32_t* dev_status, void* stream);
+
+/* Decode attention over a cache of either format: kin_sparse_decode_attn's
+ * definition on the rows' values.  sel_idx and sel_cnt NULL with k_blocks 0
+ * attend to every block; otherwise as in kin_sparse_decode_attn.  acc
+ * ([B][Hkv][Lcap] fp32), when not NULL, receives each attended token's weight
+ * summed over the group's query heads:
+ *   acc[b][h][t] += sum_{j of h} e^{z_jt - lse_j}.
+ * A block listed twice is attended to, and weighed, twice.  Weights are
+ * rounded to 11 (4 bit) or 16 (bf16) bits before they meet the values; sums
+ * are fp32.  NaN logits or values give NaN outputs.  A length outside
+ * [1, Lcap] gets out = 0, lse = -inf and flags KIN_ERR_DEVICE_DATA.
+ * workspace: kin_kv_attn_workspace_bytes for the same k_blocks (with_acc 1
+ * where acc is given), 256-byte aligned and zero-filled before its first use
+ * like kin_workspace_bytes'; with k_blocks >= 2 it serves the select calls
+ * as well.  0 bytes: invalid dims or k_blocks 1 or below 0. */
+size_t kin_kv_attn_workspace_bytes(const kin_dims* dims, int32_t k_blocks, int32_t with_acc);
+
+kin_status kin_kv_decode_attn(const kin_dims* dims, const void* q, const kin_kv* kv, const int32_t* seq_lens,
+                              const int32_t* sel_idx, const int32_t* sel_cnt, int32_t k_blocks,
+                              float softmax_scale, void* out, float* lse, float* acc, void* workspace,
+                              size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* Eviction by accumulated attention weight, for every (b, h) on its own: of
+ * the seq_lens[b] tokens the first n_sink, the last n_recent and, of the
+ * others, those with the largest acc stay (ties to the lower index; NaN
+ * counts as the lowest, -0 as 0), n_keep in all, or every token when there
+ * are no more.  Their rows move, in order, to rows 0, 1, ... of dst, a cache
+ * of the same format with its own dims (all but max_seq_len equal) and its
+ * own memory (another buffer, or pages of the same pool that no sequence
+ * still reads: a page in both block tables is undefined).  dst_lens[b] =
+ * min(seq_lens[b], n_keep); dst_acc ([B][Hkv][dst Lcap], may be NULL) takes
+ * the kept weights and zeros behind them; sel_tokens ([B][Hkv][n_keep], may
+ * be NULL) the kept tokens' old indices, ascending, -1 padded; block_means
+ * (may be NULL) the means of dst's blocks.  dst rows behind dst_lens[b] are
+ * left as they were.  The keys keep the positions they were rotated for; a
+ * later token's position is the caller's to count.
+ * A length outside [0, Lcap] keeps nothing and is flagged; a row whose page
+ * index (either side) is bad is left as it was and flagged.  n_keep < 1, or
+ * n_sink + n_recent > n_keep: KIN_ERR_INVALID_ARG; n_keep beyond either
+ * max_seq_len: KIN_ERR_CAPACITY.  workspace: kin_kv_evict_workspace_bytes
+ * (256-byte aligned, no zeroing needed). */
+size_t kin_kv_evict_workspace_bytes(const kin_dims* dims, int32_t n_keep);
+
+kin_status kin_kv_evict(const kin_dims* dims, const kin_kv* kv, const float* acc, const int32_t* seq_lens,
+                        int32_t n_keep, int32_t n_sink, int32_t n_recent, const kin_dims* dst_dims,
+                        const kin_kv* dst, float* dst_acc, int32_t* dst_lens, void* block_means,
+                        int32_t means_dtype, int32_t* sel_tokens, void* workspace, size_t ws_bytes,
+                        int32_t* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
