@@ -623,6 +623,8 @@ kin_status kv_view(const kin_dims& d, const kin_kv* kv, KvView* out) {
   if (kv->block_table) {
     kin_status st = check_pages(d, kv->k, kv->num_pages, kv->block_table, &out->pages);
     if (st != KIN_OK) return st;
+    // rows are numbered in 32 bits
+    if ((int64_t)kv->num_pages * d.num_kv_heads * d.block_size >= (int64_t)1 << 31) return KIN_ERR_CAPACITY;
   }
   out->k = static_cast<uint8_t*>(kv->k);
   out->v = static_cast<uint8_t*>(kv->v);
@@ -651,7 +653,7 @@ kin_status means_layout(const kin_dims& d, const KvView& kv, const void* means, 
 bool same_cache(const KvView& a, const KvView& b) { return a.k == b.k || a.v == b.v || a.k == b.v || a.v == b.k; }
 
 #ifndef KIN_KV4_CHUNK_TOKENS
-#define KIN_KV4_CHUNK_TOKENS 768
+#define KIN_KV4_CHUNK_TOKENS 2048
 #endif
 
 // Kept blocks per attention CTA: 768 tokens (110 KB of 4-bit rows), fewer
@@ -661,8 +663,10 @@ int kv_chunk_blocks(const kin_dims& d, int k) {
   const int64_t by_grid = (int64_t)k * pairs_of(d) / (2 * kTargetSMs);
   int ch = by_tokens;
   if (by_grid < ch) ch = by_grid > 0 ? (int)by_grid : 1;
-  const int cap = kMaxItemTiles / (d.block_size / kTileTokens);
-  return ch < cap ? ch : cap;
+  const int cap = kKvItemTiles / (d.block_size / kTileTokens);
+  if (ch > cap) ch = cap;
+  const int chunks = (k + ch - 1) / ch;  // chunks of even length
+  return (k + chunks - 1) / chunks;
 }
 
 // The slots of the kept blocks of a pair: at most k_blocks, at most all.

@@ -326,6 +326,7 @@ struct TokenParams {
 // A cache as kin_kv describes it.  INT4 rows: kCodeBytes bytes of codes and
 // kGroups bf16 scales, one per kGroupDim channels (see kin.h).
 constexpr int kGroupDim = 32;
+constexpr int kKvItemTiles = 128;  // attention tiles per work item (32 per warp, one per lane)
 constexpr int kGroups = kHeadDim / kGroupDim;
 constexpr int kCodeBytes = kHeadDim / 2;
 

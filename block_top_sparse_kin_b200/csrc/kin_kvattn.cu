@@ -25,6 +25,9 @@ namespace {
 
 #define kNegInf (-__int_as_float(0x7f800000))
 
+#ifndef KIN_KV4_CTAS_PER_SM
+#define KIN_KV4_CTAS_PER_SM 4
+#endif
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRowPad = kHeadDim + 4;
@@ -36,7 +39,10 @@ struct Ring {
   // 64 bytes of key codes, of value codes, then 16 x 4 scales of each.
   static constexpr int kStageBytes = kInt4 ? 2 * 16 * kCodeBytes + 2 * 16 * kGroups * 2 : 4 * kHalfBox;
   static constexpr int kStages = kInt4 ? 4 : 2;
-  static constexpr int kPipe = kWarps * kStages * kStageBytes;
+  // 4 bit, per warp behind the ring: the tile's key scales as fp32 [16][4] and
+  // its value scales as fp16 pairs [8 token pairs][4]
+  static constexpr int kScaleBytes = kInt4 ? 256 + 128 : 0;
+  static constexpr int kPipe = kWarps * (kStages * kStageBytes + kScaleBytes);
   static constexpr int kComb = kWarps * kMaxGroup * kRowPad * 4;
   static constexpr int kSmem = (kPipe > kComb ? kPipe : kComb) + 1024;
 };
@@ -60,16 +66,65 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return d;
 }
 
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+// D = A B + C with C left as it is
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
+}
+
+__device__ __forceinline__ unsigned count_chunk(uint32_t* counter) {
+  unsigned v;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(counter) : "memory");
+  return v;
+}
+
+// 2^x to 2^-22, results below 2^-126 as zero: a weight that small adds nothing
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void sts64(uint32_t a, float x, float y) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
@@ -86,50 +141,61 @@ __device__ __forceinline__ uint32_t tok_mask(int t, int nvalid) {
   return (t < nvalid ? 0x0000FFFFu : 0u) | (t + 1 < nvalid ? 0xFFFF0000u : 0u);
 }
 
-// The product sums' state of a warp: O^T fragments, running maximum and sum
-// of its two head columns.
+// A head's weights are 2^(z - r) with a reference r that follows the running
+// maximum m of its logits loosely: r = m - kLead, and m moves (all sums are
+// then rescaled) only when a logit passes m + kSlack.  So a tile usually
+// costs no reduction over its tokens, and a weight is at most
+// 2^(kLead + kSlack) = 2^14, inside fp16.
+constexpr float kLead = 6.f, kSlack = 8.f;
+
+// The sums of a warp: O^T fragments, and for its two head columns the maximum
+// logit followed, before the scaling to base 2 (raw), the reference and the
+// weights' sum.
 struct Acc {
   float o[8][4];
-  float m0, m1, l0, l1;
+  float sums[4];  // 4 bit: row G < 4 holds the weights' sums p vs of group G
+  float m[2], thr[2], r[2], l[2];
 };
 
-// Running maximum over the tile and the tile's weights; rescales the sums
-// when some maximum grew (then the whole warp does).  s holds the base-2
-// logits (rows tq, tq + 8; heads ta, ta + 1), -inf where there is no token.
-__device__ __forceinline__ void online_softmax(Acc& a, const float (&s)[4], float (&p)[4]) {
-  float x0 = fmaxf(s[0], s[2]), x1 = fmaxf(s[1], s[3]);
+// The tile's weights p from its raw logits s (rows tq, tq + 8; heads ta,
+// ta + 1; -inf where there is no token); sl2: base-2 scale of the two heads.
+__device__ __forceinline__ void weigh(Acc& a, const float (&s)[4], const float (&sl2)[2], float (&p)[4]) {
+  const float x0 = fmaxf(s[0], s[2]), x1 = fmaxf(s[1], s[3]);
+  if (__any_sync(0xffffffffu, x0 > a.thr[0] || x1 > a.thr[1])) {
+    float x[2] = {x0, x1};
 #pragma unroll
-  for (int off = 4; off < 32; off <<= 1) {
-    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
-    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
-  }
-  const float mn0 = fmaxf(a.m0, x0), mn1 = fmaxf(a.m1, x1);
-  if (__any_sync(0xffffffffu, mn0 != a.m0 || mn1 != a.m1)) {
-    const float al0 = exp2f(a.m0 - mn0), al1 = exp2f(a.m1 - mn1);
-    a.l0 *= al0;
-    a.l1 *= al1;
-#pragma unroll
-    for (int dm = 0; dm < 8; ++dm) {
-      a.o[dm][0] *= al0;
-      a.o[dm][1] *= al1;
-      a.o[dm][2] *= al0;
-      a.o[dm][3] *= al1;
+    for (int off = 4; off < 32; off <<= 1) {
+      x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], off));
+      x[1] = fmaxf(x[1], __shfl_xor_sync(0xffffffffu, x[1], off));
     }
-    a.m0 = mn0;
-    a.m1 = mn1;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float mn = fmaxf(a.m[j], x[j]);
+      const float al = mn == a.m[j] ? 1.f : exp2_approx((a.m[j] - mn) * sl2[j]);
+      a.m[j] = mn;
+      a.thr[j] = mn + __fdividef(kSlack, sl2[j]);
+      a.r[j] = mn * sl2[j] - kLead;
+      a.l[j] *= al;
+      a.sums[j] *= al;
+      a.sums[2 + j] *= al;
+#pragma unroll
+      for (int dm = 0; dm < 8; ++dm) {
+        a.o[dm][j] *= al;
+        a.o[dm][2 + j] *= al;
+      }
+    }
   }
-  p[0] = exp2f(s[0] - a.m0);
-  p[1] = exp2f(s[1] - a.m1);
-  p[2] = exp2f(s[2] - a.m0);
-  p[3] = exp2f(s[3] - a.m1);
-  a.l0 += p[0] + p[2];
-  a.l1 += p[1] + p[3];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    p[i] = exp2_approx(fmaf(s[i], sl2[i & 1], -a.r[i & 1]));
+    a.l[i & 1] += p[i];
+  }
 }
 
 }  // namespace
 
 template <bool kInt4, bool kAcc>
-__global__ void __launch_bounds__(kThreads, kInt4 ? 4 : 3) kv_attn_kernel(KvAttnParams p) {
+__global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_attn_kernel(KvAttnParams p) {
   using R = Ring<kInt4>;
   constexpr int kStages = R::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -179,9 +245,12 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? 4 : 3) kv_attn_kernel(KvAttn
   }
   if (ntiles == 0) return;
 
-  // this warp's tiles t = warp + W n; lane n holds tile n's row and valid rows
+  // this warp's tiles t = warp + W n; lane n holds tile n's first row (a cache
+  // of 2^31 rows is larger than the memory) and its valid rows; kPartial marks
+  // a tile of less than 16
+  constexpr uint32_t kPartial = 0x80000000u;
   const int n_w = warp < ntiles ? (ntiles - 1 - warp) / kWarps + 1 : 0;
-  int64_t my_row = 0;
+  uint32_t my_row = kPartial;
   int my_nvalid = 0;
   if (lane < n_w) {
     const int t = warp + kWarps * lane;
@@ -190,133 +259,223 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? 4 : 3) kv_attn_kernel(KvAttn
     if (blk >= 0 && blk < nb && tok < L) row = kv_row(p.kv.pages, b, h, p.Hkv, Lcap, bs, tok);
     if (blk < 0 || blk >= nb || (tok < L && row < 0)) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
     my_nvalid = row < 0 ? 0 : min(kTileTokens, L - tok);
-    my_row = row < 0 ? 0 : row;
+    my_row = (row < 0 ? 0u : (uint32_t)row) | (my_nvalid < kTileTokens ? kPartial : 0u);
   }
 
-  // Q fragments (B operand): head n = lane / 4; channels by the tile's order
+  // Q fragments (B operand): head n = lane / 4.  sl2: the base-2 scale of the
+  // raw logits of heads ta and ta + 1.
   uint32_t qf[8][2];
   const int n = lane >> 2, c = lane & 3;
-  {
-    const uint32_t* qrow = reinterpret_cast<const uint32_t*>(p.q + (qh0 + (n < g ? n : 0)) * kHeadDim);
+  const int tq = lane >> 2, ta = 2 * c;
+  float sl2[2] = {p.scale_log2, p.scale_log2};
+  // 4 bit: key nibbles enter the first product as the fp16 numbers n 2^-24
+  // (bits 0..3 of a half) and n 2^-20 (bits 4..7): one AND for two, no
+  // conversion.  So q is fp16 too, each head scaled by a power of two to a
+  // largest magnitude in [2^14, 2^15): its 8 bits are kept exactly down to
+  // 2^-31 of that, and what is lost below is under fp32's own rounding.  The
+  // channels met by n 2^-20 are scaled by 2^-4 more.  A nibble is c + 8: each
+  // group's sum starts at -8 times its sum of q, from a product with ones.
+  float qs[4][4];
+  const __nv_bfloat16* qrow = p.q + (qh0 + (n < g ? n : 0)) * kHeadDim;
+  if constexpr (kInt4) {
+    uint4 w[4];
+    uint32_t mx = 0;
+#pragma unroll
+    for (int G = 0; G < 4; ++G) {
+      w[G] = __ldg(reinterpret_cast<const uint4*>(qrow + 32 * G + 8 * c));
+      if (n >= g) w[G] = make_uint4(0u, 0u, 0u, 0u);
+      mx = max_u16x2(mx, max_u16x2(max_u16x2(w[G].x & 0x7FFF7FFFu, w[G].y & 0x7FFF7FFFu),
+                                   max_u16x2(w[G].z & 0x7FFF7FFFu, w[G].w & 0x7FFF7FFFu)));
+    }
+    mx = max(mx & 0xFFFFu, mx >> 16);
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const uint32_t e = mx >> 7;  // biased exponent of the largest magnitude
+    const uint32_t fe = e == 255u || mx == 0u ? 127u : min(268u - e, 254u);
+    const float f = __uint_as_float(fe << 23);  // 2^(fe - 127)
+    const float undo = p.scale_log2 * __uint_as_float(min(278u - fe, 254u) << 23);  // 2^24 / f
+#pragma unroll
+    for (int j = 0; j < 2; ++j) sl2[j] = __shfl_sync(0xffffffffu, undo, 4 * (ta + j));
+    const float f4 = f * 0x1p-4f;
+#pragma unroll
+    for (int G = 0; G < 4; ++G) {
+      const uint32_t v[4] = {w[G].x, w[G].y, w[G].z, w[G].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float fi = (i & 1) ? f4 : f;
+        qf[2 * G + (i >> 1)][i & 1] = pack_f16x2(lo_f(v[i]) * fi, hi_f(v[i]) * fi);
+      }
+      // ones for the first channels of a step, 2^4 for the scaled ones
+      qs[G][0] = qs[G][1] = qs[G][2] = qs[G][3] = 0.f;
+      mma_f16_16816(qs[G], 0x3C003C00u, 0x3C003C00u, 0x4C004C00u, 0x4C004C00u, qf[2 * G][0], qf[2 * G][1]);
+      mma_f16_16816(qs[G], 0x3C003C00u, 0x3C003C00u, 0x4C004C00u, 0x4C004C00u, qf[2 * G + 1][0], qf[2 * G + 1][1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qs[G][i] *= -0x1p-21f;  // -8 * 2^-24
+    }
+  } else {
+    const uint32_t* q32 = reinterpret_cast<const uint32_t*>(qrow);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
-      if constexpr (kInt4) {  // k slots 2c.. of step 2G + e: channels 32 G + 8 c + 4 e ..
-        const int w = (kk >> 1) * 16 + 4 * c + 2 * (kk & 1);
-        qf[kk][0] = n < g ? __ldg(qrow + w) : 0u;
-        qf[kk][1] = n < g ? __ldg(qrow + w + 1) : 0u;
-      } else {
-        qf[kk][0] = n < g ? __ldg(qrow + kk * 8 + c) : 0u;
-        qf[kk][1] = n < g ? __ldg(qrow + kk * 8 + 4 + c) : 0u;
-      }
+      qf[kk][0] = n < g ? __ldg(q32 + kk * 8 + c) : 0u;
+      qf[kk][1] = n < g ? __ldg(q32 + kk * 8 + 4 + c) : 0u;
     }
   }
 
-  const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kStages * R::kStageBytes);
-  auto issue = [&](int nt) {
-    const int64_t row = (int64_t)(((uint64_t)(uint32_t)__shfl_sync(0xffffffffu, (int)(my_row >> 32), nt & 31) << 32) |
-                                  (uint32_t)__shfl_sync(0xffffffffu, (int)(uint32_t)my_row, nt & 31));
-    const int nv = __shfl_sync(0xffffffffu, my_nvalid, nt & 31);
-    if (nt < n_w && nv > 0) {
-      const uint32_t base = ring + (uint32_t)((nt % kStages) * R::kStageBytes);
+  const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * (kStages * R::kStageBytes + R::kScaleBytes));
+  const uint32_t scales = ring + kStages * R::kStageBytes;
+  // 4 bit: 64 pieces of 16 bytes of key codes and of value codes, 8 bytes of
+  // scales for each row.  Key row i of the tile holds token (i & 8) + 4 (i & 1)
+  // + (i & 7) / 2, so that the tile's k slots 2c, 2c + 1 of the second product
+  // are tokens c, c + 4 (and 8 + c, 12 + c); the value rows stay in token
+  // order, their pieces 2 and 3 swapped with 0 and 1 in every second pair of
+  // rows, which keeps their 8-byte reads free of bank conflicts.
+  const int it = lane >> 2, icol = lane & 3;
+  const uint32_t k_dst = ring + (((it & 3) << 1) | (it >> 2)) * 64 + icol * 16;
+  const uint32_t v_dst = ring + 1024 + it * 64 + ((icol ^ (it & 2)) << 4);
+  const uint32_t s_dst = ring + 2048 + lane * 8;
+  const uint8_t* k_src = p.kv.k + lane * 16;
+  const uint8_t* v_src = p.kv.v + lane * 16;
+  const uint16_t* s_src = (lane < 16 ? p.kv.ks : p.kv.vs) + (lane & 15) * kGroups;
+  auto issue = [&](int nt, uint32_t slot) {  // slot: byte offset of the ring slot
+    const uint32_t row = nt < n_w ? __shfl_sync(0xffffffffu, my_row, nt & 31) : kPartial;
+    if (row < kPartial) {
       if constexpr (kInt4) {
-        // 64 pieces of 16 bytes of key codes and of value codes.  Key row i of
-        // the tile holds token (i & 8) + 4 (i & 1) + (i & 7) / 2, so that the
-        // tile's k slots 2c, 2c + 1 of the second product are tokens c, c + 4
-        // (and 8 + c, 12 + c); the value rows stay in token order, their
-        // pieces 2 and 3 swapped with 0 and 1 in every second pair of rows.
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int t = (lane >> 2) + 8 * i, col = lane & 3;
-          const int kr = (t & 8) | ((t & 3) << 1) | ((t >> 2) & 1);
-          const int64_t src = (row + (t < nv ? t : 0)) * kCodeBytes + col * 16;
-          const uint32_t bytes = t < nv ? 16u : 0u;
-          cp_async16(base + kr * 64 + col * 16, p.kv.k + src, bytes);
-          cp_async16(base + 1024 + t * 64 + ((col ^ (t & 2)) << 4), p.kv.v + src, bytes);
-        }
-        const int t = lane & 15;
-        const uint16_t* sc = (lane < 16 ? p.kv.ks : p.kv.vs) + (row + (t < nv ? t : 0)) * kGroups;
-        cp_async8(base + 2048 + lane * 8, sc, t < nv ? 8u : 0u);
+        const uint8_t* ks = k_src + (uint64_t)row * kCodeBytes;
+        const uint8_t* vs = v_src + (uint64_t)row * kCodeBytes;
+        cp_async16(k_dst + slot, ks, 16u);
+        cp_async16(k_dst + slot + 512, ks + 512, 16u);
+        cp_async16(v_dst + slot, vs, 16u);
+        cp_async16(v_dst + slot + 512, vs + 512, 16u);
+        cp_async8(s_dst + slot, s_src + (uint64_t)row * kGroups, 8u);
       } else {
-        const int64_t off0 = row * kHeadDim;
-        const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.kv.k);
-        const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.kv.v);
+        const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.kv.k) + (uint64_t)row * kHeadDim;
+        const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.kv.v) + (uint64_t)row * kHeadDim;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int piece = lane + 32 * i;
           const int r = piece >> 4, cc = piece & 15;
-          const uint32_t off = (uint32_t)((cc >> 3) * kHalfBox + r * 128 + (((cc & 7) ^ (r & 7)) << 4));
-          const int64_t src = off0 + (int64_t)(r < nv ? r : 0) * kHeadDim + cc * 8;
-          const uint32_t bytes = r < nv ? 16u : 0u;
-          cp_async16(base + off, k + src, bytes);
-          cp_async16(base + 2 * kHalfBox + off, v + src, bytes);
+          const uint32_t off = ring + slot + (uint32_t)((cc >> 3) * kHalfBox + r * 128 + (((cc & 7) ^ (r & 7)) << 4));
+          cp_async16(off, k + piece * 8, 16u);
+          cp_async16(off + 2 * kHalfBox, v + piece * 8, 16u);
+        }
+      }
+    } else if (nt < n_w) {  // rows behind the length: zeros, nothing read (the address stays on a valid row)
+      const int nv = __shfl_sync(0xffffffffu, my_nvalid, nt & 31);
+      const uint64_t r0 = row & ~kPartial;
+      if (nv > 0) {
+        if constexpr (kInt4) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int t = it + 8 * i;
+            const int64_t from = (int64_t)r0 * kCodeBytes + (t < nv ? 512 * i : -it * 64);
+            cp_async16(k_dst + slot + 512 * i, k_src + from, t < nv ? 16u : 0u);
+            cp_async16(v_dst + slot + 512 * i, v_src + from, t < nv ? 16u : 0u);
+          }
+          const int t = lane & 15;
+          cp_async8(s_dst + slot, s_src + (int64_t)r0 * kGroups - (t < nv ? 0 : t * kGroups), t < nv ? 8u : 0u);
+        } else {
+          const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.kv.k) + r0 * kHeadDim;
+          const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.kv.v) + r0 * kHeadDim;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int piece = lane + 32 * i;
+            const int r = piece >> 4, cc = piece & 15;
+            const uint32_t off = ring + slot + (uint32_t)((cc >> 3) * kHalfBox + r * 128 + (((cc & 7) ^ (r & 7)) << 4));
+            const int src = (r < nv ? r : 0) * kHeadDim + cc * 8;
+            const uint32_t bytes = r < nv ? 16u : 0u;
+            cp_async16(off, k + src, bytes);
+            cp_async16(off + 2 * kHalfBox, v + src, bytes);
+          }
         }
       }
     }
     cp_async_commit();  // one group per tile, empty or not
   };
 #pragma unroll
-  for (int i = 0; i < kStages; ++i) issue(i);
+  for (int i = 0; i < kStages; ++i) issue(i, i * R::kStageBytes);
 
   Acc a;
 #pragma unroll
   for (int dm = 0; dm < 8; ++dm) a.o[dm][0] = a.o[dm][1] = a.o[dm][2] = a.o[dm][3] = 0.f;
-  a.m0 = a.m1 = kNegInf;
-  a.l0 = a.l1 = 0.f;
-  const float sl2 = p.scale_log2;
-  const int tq = lane >> 2, ta = 2 * c;
-
-  // 4 bit: the codes enter the first product as 24 + c (16 + nibble, one
-  // shift and one logic operation for two); each group's sum starts at -24
-  // times the sum of its query channels, from a product with ones.
-  float qs[4][2];
-  // the second product's weights p vs are held in fp16 (11 bits; a bf16 weight
-  // would cost as much accuracy as the final rounding), scaled by 2^14 / vn,
-  // vn a power of two above the warp's largest value scale so far
-  uint32_t vn_bits = 27u << 23;  // 2^-100
-  float kf = 0x1p114f;
-  if constexpr (kInt4) {
-#pragma unroll
-    for (int G = 0; G < 4; ++G) {
-      float one[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_bf16_16816(one, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, qf[2 * G][0], qf[2 * G][1]);
-      mma_bf16_16816(one, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, qf[2 * G + 1][0], qf[2 * G + 1][1]);
-      qs[G][0] = -24.f * one[0];
-      qs[G][1] = -24.f * one[1];
-    }
-  }
+  a.sums[0] = a.sums[1] = a.sums[2] = a.sums[3] = 0.f;
+  a.m[0] = a.m[1] = a.thr[0] = a.thr[1] = a.r[0] = a.r[1] = kNegInf;
+  a.l[0] = a.l[1] = 0.f;
+  // 4 bit: the second product's weights p vs are fp16 (11 bits; a bf16 weight
+  // would cost as much accuracy as the final rounding): p, and vs divided by
+  // vn, a power of two above the group's largest scale in this warp so far (at
+  // least 2^-100).  Lane l keeps the vn of group l % 4.
+  uint32_t vn_bits = 27u << 23;
+  float inv_vn = 0x1p100f;
+  bool v_nan = false;
+  uint32_t slot = 0;
 
   for (int nt = 0; nt < n_w; ++nt) {
     cp_async_wait<kStages - 1>();
     __syncwarp();
-    const int nvalid = __shfl_sync(0xffffffffu, my_nvalid, nt & 31);
+    int nvalid = kTileTokens;
+    if (__shfl_sync(0xffffffffu, my_row, nt & 31) & kPartial) nvalid = __shfl_sync(0xffffffffu, my_nvalid, nt & 31);
     if (nvalid > 0) {
-      const uint32_t base = ring + (uint32_t)((nt % kStages) * R::kStageBytes);
+      const uint32_t base = ring + slot;
       float s[4], pr[4];
       int t0, t1;  // the tokens of this lane's logits
       if constexpr (kInt4) {
         const uint4 wa = lds128(base + lane * 16), wb = lds128(base + 512 + lane * 16);
+        {
+          // the tile's scales, each unpacked once for the warp: lane l the key
+          // scales of token l / 2, groups 2 (l % 2) and the next; and group
+          // l % 4's value scales of token pair l / 4 (tokens tp, tp + 4)
+          const uint32_t kw = lds32(base + 2048 + lane * 4);
+          const int tp = (it & 3) + 8 * (it >> 2);
+          float v0 = __uint_as_float(lds16(base + 2176 + tp * 8 + icol * 2) << 16);
+          float v1 = __uint_as_float(lds16(base + 2176 + tp * 8 + 32 + icol * 2) << 16);
+          sts64(scales + lane * 8, lo_f(kw), hi_f(kw));
+          float vn = __uint_as_float(vn_bits);
+          if (__any_sync(0xffffffffu, !(v0 < vn) || !(v1 < vn))) {
+            // a scale that is not finite makes its group NaN whatever its
+            // weight: noted here, and kept out of the products
+            v_nan |= !(v0 < 0x1p127f) || !(v1 < 0x1p127f);
+            if (!(v0 < 0x1p127f)) v0 = 0.f;
+            if (!(v1 < 0x1p127f)) v1 = 0.f;
+            // a larger one moves the group's sums to its power of two
+            uint32_t mb = __float_as_uint(fmaxf(v0, v1));
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, off));
+            const uint32_t e = mb >= vn_bits ? min((mb >> 23) + 1u, 253u) : vn_bits >> 23;
+            inv_vn = __uint_as_float((254u - e) << 23);
+            const float down = vn * inv_vn;
+            vn_bits = e << 23;
+            const float mine = __shfl_sync(0xffffffffu, down, tq & 3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a.sums[i] *= mine;
+#pragma unroll
+            for (int dm = 0; dm < 8; ++dm) {
+              const float dg = __shfl_sync(0xffffffffu, down, dm >> 1);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) a.o[dm][i] *= dg;
+            }
+          }
+          sts32(scales + 256 + lane * 4, pack_f16x2(v0 * inv_vn, v1 * inv_vn));
+        }
+        __syncwarp();
         const uint32_t ka[4] = {wa.x, wa.y, wa.z, wa.w}, kb[4] = {wb.x, wb.y, wb.z, wb.w};
         t0 = ((tq & 1) << 2) | (tq >> 1);
         t1 = t0 + 8;
-        const uint2 sa = lds64(base + 2048 + t0 * 8), sb = lds64(base + 2048 + t1 * 8);
-        s[0] = s[1] = s[2] = s[3] = 0.f;
+        const uint4 sa = lds128(scales + t0 * 16), sb = lds128(scales + t1 * 16);
+        const float fa4[4] = {__uint_as_float(sa.x), __uint_as_float(sa.y), __uint_as_float(sa.z), __uint_as_float(sa.w)};
+        const float fb4[4] = {__uint_as_float(sb.x), __uint_as_float(sb.y), __uint_as_float(sb.z), __uint_as_float(sb.w)};
 #pragma unroll
         for (int G = 0; G < 4; ++G) {
-          auto pair_of = [](uint32_t w, int i) {
-            const uint32_t x = i == 0 ? w << 3 : w >> (4 * i - 3);
-            return (x & 0x00780078u) | 0x41804180u;
-          };
-          float d[4] = {qs[G][0], qs[G][1], qs[G][0], qs[G][1]};
-          mma_bf16_16816(d, pair_of(ka[G], 0), pair_of(kb[G], 0), pair_of(ka[G], 1), pair_of(kb[G], 1), qf[2 * G][0],
-                         qf[2 * G][1]);
-          mma_bf16_16816(d, pair_of(ka[G], 2), pair_of(kb[G], 2), pair_of(ka[G], 3), pair_of(kb[G], 3),
-                         qf[2 * G + 1][0], qf[2 * G + 1][1]);
-          const uint32_t wsa = G < 2 ? sa.x : sa.y, wsb = G < 2 ? sb.x : sb.y;
-          const float fa = (G & 1) ? hi_f(wsa) : lo_f(wsa), fb = (G & 1) ? hi_f(wsb) : lo_f(wsb);
-          s[0] = fmaf(fa, d[0], s[0]);
-          s[1] = fmaf(fa, d[1], s[1]);
-          s[2] = fmaf(fb, d[2], s[2]);
-          s[3] = fmaf(fb, d[3], s[3]);
+          float d[4];
+          const uint32_t ha = ka[G] >> 8, hb = kb[G] >> 8;
+          mma_f16_from(d, qs[G], ka[G] & 0x000F000Fu, kb[G] & 0x000F000Fu, ka[G] & 0x00F000F0u, kb[G] & 0x00F000F0u,
+                       qf[2 * G][0], qf[2 * G][1]);
+          mma_f16_16816(d, ha & 0x000F000Fu, hb & 0x000F000Fu, ha & 0x00F000F0u, hb & 0x00F000F0u, qf[2 * G + 1][0],
+                        qf[2 * G + 1][1]);
+          const float fa = fa4[G], fb = fb4[G];
+          s[0] = G ? fmaf(fa, d[0], s[0]) : fa * d[0];
+          s[1] = G ? fmaf(fa, d[1], s[1]) : fa * d[1];
+          s[2] = G ? fmaf(fb, d[2], s[2]) : fb * d[2];
+          s[3] = G ? fmaf(fb, d[3], s[3]) : fb * d[3];
         }
       } else {
         t0 = tq;
@@ -337,56 +496,34 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? 4 : 3) kv_attn_kernel(KvAttn
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] = sa[i] + sb[i];
       }
-      const bool v0 = t0 < nvalid, v1 = t1 < nvalid;
-      s[0] = v0 ? s[0] * sl2 : kNegInf;
-      s[1] = v0 ? s[1] * sl2 : kNegInf;
-      s[2] = v1 ? s[2] * sl2 : kNegInf;
-      s[3] = v1 ? s[3] * sl2 : kNegInf;
+      if (nvalid < kTileTokens) {
+        if (t0 >= nvalid) s[0] = s[1] = kNegInf;
+        if (t1 >= nvalid) s[2] = s[3] = kNegInf;
+      }
       if constexpr (kAcc) {  // the logits of the tile, for the weights once lse is known
         const int64_t slot = pair * p.k * bs + (int64_t)(j0 * tpb + warp + kWarps * nt) * kTileTokens;
         float* z0 = p.z + (slot + t0) * g + ta;
         float* z1 = p.z + (slot + t1) * g + ta;
         if (ta < g) {
-          z0[0] = s[0];
-          z1[0] = s[2];
+          z0[0] = s[0] * sl2[0];
+          z1[0] = s[2] * sl2[0];
         }
         if (ta + 1 < g) {
-          z0[1] = s[1];
-          z1[1] = s[3];
+          z0[1] = s[1] * sl2[1];
+          z1[1] = s[3] * sl2[1];
         }
       }
-      online_softmax(a, s, pr);
+      weigh(a, s, sl2, pr);
       if constexpr (kInt4) {
-        const uint2 sa = lds64(base + 2048 + 128 + t0 * 8), sb = lds64(base + 2048 + 128 + t1 * 8);
-        float fa[4] = {lo_f(sa.x), hi_f(sa.x), lo_f(sa.y), hi_f(sa.y)};
-        float fb[4] = {lo_f(sb.x), hi_f(sb.x), lo_f(sb.y), hi_f(sb.y)};
-        // fmaxf drops NaN scales: they reach the output through the weights
-        const float mx = fmaxf(fmaxf(fmaxf(fa[0], fa[1]), fmaxf(fa[2], fa[3])),
-                               fmaxf(fmaxf(fb[0], fb[1]), fmaxf(fb[2], fb[3])));
-        const uint32_t mb = __reduce_max_sync(0xffffffffu, mx > 0.f ? __float_as_uint(mx) : 0u);
-        if (mb >= vn_bits) {  // warp-uniform: a larger scale, the sums move to its power of two
-          const uint32_t e = min((mb >> 23) + 1u, 253u);
-          const float down = __uint_as_float(vn_bits) * __uint_as_float((254u - e) << 23);  // old vn / new vn
-#pragma unroll
-          for (int dm = 0; dm < 8; ++dm) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a.o[dm][i] *= down;
-          }
-          vn_bits = e << 23;
-          kf = __uint_as_float((254u - e) << 23) * 0x1p14f;
-        }
-        float pk[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pk[i] = pr[i] * kf;
-        uint32_t pb[4][2];
-#pragma unroll
-        for (int G = 0; G < 4; ++G) {
-          pb[G][0] = movmatrix_trans(pack_f16x2(pk[0] * fa[G], pk[1] * fa[G]));
-          pb[G][1] = movmatrix_trans(pack_f16x2(pk[2] * fb[G], pk[3] * fb[G]));
-        }
-        // value codes: tokens c, c + 4, c + 8, c + 12; lane's 4 channels of
-        // each group.  Two tokens' halfwords side by side, then a nibble of
-        // each as 1024 + n (or 1024 + 16 n) in fp16, brought to n - 8 exactly.
+        const uint32_t p0 = movmatrix_trans(pack_f16x2(pr[0], pr[1])), p1 = movmatrix_trans(pack_f16x2(pr[2], pr[3]));
+        const uint4 va = lds128(scales + 256 + c * 16), vb = lds128(scales + 256 + 64 + c * 16);
+        const uint32_t pb[4][2] = {{hmul2(p0, va.x), hmul2(p1, vb.x)}, {hmul2(p0, va.y), hmul2(p1, vb.y)},
+                                   {hmul2(p0, va.z), hmul2(p1, vb.z)}, {hmul2(p0, va.w), hmul2(p1, vb.w)}};
+        // value codes: tokens c, c + 4, c + 8, c + 12; the lane's 4 channels of
+        // each group.  Two tokens' halfwords side by side, then nibbles as
+        // n 2^-24 and n 2^-20 like the keys'; 8 times the weights' sum, taken
+        // by a product with a row of ones for each group, comes off at the
+        // end (a warp's tiles are few enough for it to cost nothing).
         uint2 x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -398,13 +535,13 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? 4 : 3) kv_attn_kernel(KvAttn
           const uint32_t sel = (G & 1) ? 0x7632u : 0x5410u;
           const uint32_t u01 = __byte_perm(G < 2 ? x[0].x : x[0].y, G < 2 ? x[1].x : x[1].y, sel);
           const uint32_t u23 = __byte_perm(G < 2 ? x[2].x : x[2].y, G < 2 ? x[3].x : x[3].y, sel);
-          auto nib = [](uint32_t u, int i) {
-            const uint32_t v = i & 2 ? u >> 8 : u;
-            return (i & 1) ? hfma2((v & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u)   // x / 16 - 72
-                           : hfma2((v & 0x000F000Fu) | 0x64006400u, 0x3C003C00u, 0xE408E408u);  // x - 1032
-          };
-          mma_f16_16816(a.o[2 * G], nib(u01, 0), nib(u01, 1), nib(u23, 0), nib(u23, 1), pb[G][0], pb[G][1]);
-          mma_f16_16816(a.o[2 * G + 1], nib(u01, 2), nib(u01, 3), nib(u23, 2), nib(u23, 3), pb[G][0], pb[G][1]);
+          const uint32_t h01 = u01 >> 8, h23 = u23 >> 8;
+          const uint32_t one = tq == G ? 0x3C003C00u : 0u;
+          mma_f16_16816(a.o[2 * G], u01 & 0x000F000Fu, u01 & 0x00F000F0u, u23 & 0x000F000Fu, u23 & 0x00F000F0u, pb[G][0],
+                        pb[G][1]);
+          mma_f16_16816(a.o[2 * G + 1], h01 & 0x000F000Fu, h01 & 0x00F000F0u, h23 & 0x000F000Fu, h23 & 0x00F000F0u,
+                        pb[G][0], pb[G][1]);
+          mma_f16_16816(a.sums, one, 0u, one, 0u, pb[G][0], pb[G][1]);
         }
       } else {
         // weights as the sum of two bf16 numbers (16 bits): a single bf16
@@ -434,29 +571,38 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? 4 : 3) kv_attn_kernel(KvAttn
       }
     }
     __syncwarp();
-    issue(nt + kStages);
+    issue(nt + kStages, slot);
+    slot = slot == (kStages - 1) * R::kStageBytes ? 0u : slot + R::kStageBytes;
   }
   cp_async_wait<0>();
 
 #pragma unroll
   for (int off = 4; off < 32; off <<= 1) {
-    a.l0 += __shfl_xor_sync(0xffffffffu, a.l0, off);
-    a.l1 += __shfl_xor_sync(0xffffffffu, a.l1, off);
+    a.l[0] += __shfl_xor_sync(0xffffffffu, a.l[0], off);
+    a.l[1] += __shfl_xor_sync(0xffffffffu, a.l[1], off);
   }
   __syncthreads();  // every warp is done with its ring; the combine area reuses it
   float* comb = reinterpret_cast<float*>(smem);  // [warp][head][kRowPad]
   {
     float* w0 = comb + ((warp * kMaxGroup) + ta) * kRowPad;
     if constexpr (kInt4) {
-      // o[2G + e][..]: channel 32 G + 4 tq + 2 e (+ 1), heads ta and ta + 1
-      const float back = __uint_as_float(vn_bits) * 0x1p-14f;
+      // o[2G + e][i]: channel 32 G + 4 tq + 2 e + (i / 2), head ta + (i & 1);
+      // the weights' sums of group G sit in the lanes of row G
+      uint32_t nans = __ballot_sync(0xffffffffu, v_nan);  // bit l: group l % 4
+      nans |= nans >> 16;
+      nans |= nans >> 8;
+      nans |= nans >> 4;
 #pragma unroll
       for (int dm = 0; dm < 8; ++dm) {
         const int d = (dm >> 1) * 32 + 4 * tq + 2 * (dm & 1);
-        w0[d] = a.o[dm][0] * back;
-        w0[kRowPad + d] = a.o[dm][1] * back;
-        w0[d + 1] = a.o[dm][2] * back;
-        w0[kRowPad + d + 1] = a.o[dm][3] * back;
+        float vn = __uint_as_float(__shfl_sync(0xffffffffu, vn_bits, dm >> 1));
+        if ((nans >> (dm >> 1)) & 1u) vn = __int_as_float(0x7FFFFFFF);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float off = -8.f * __shfl_sync(0xffffffffu, a.sums[j], (dm >> 1) * 4 + c);
+          w0[j * kRowPad + d] = fmaf(a.o[dm][j], 0x1p24f, off) * vn;
+          w0[j * kRowPad + d + 1] = fmaf(a.o[dm][2 + j], 0x1p20f, off) * vn;
+        }
       }
     } else {
 #pragma unroll
@@ -470,10 +616,10 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? 4 : 3) kv_attn_kernel(KvAttn
     }
   }
   if (lane < 4) {
-    s_m[warp][2 * lane] = a.m0;
-    s_m[warp][2 * lane + 1] = a.m1;
-    s_l[warp][2 * lane] = a.l0;
-    s_l[warp][2 * lane + 1] = a.l1;
+    s_m[warp][2 * lane] = a.r[0];
+    s_m[warp][2 * lane + 1] = a.r[1];
+    s_l[warp][2 * lane] = a.l[0];
+    s_l[warp][2 * lane + 1] = a.l[1];
   }
   __syncthreads();
   if (tid < g) {  // per head: the maximum over the warps, each warp's weight, the sum
@@ -522,12 +668,12 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? 4 : 3) kv_attn_kernel(KvAttn
       part[j * kPartStride + kHeadDim + 1] = s_cden[j];
     }
   }
-  __threadfence();
+  // the barrier orders every thread's partial before thread 0's release, its
+  // acquire (of the other chunks' releases) before what the others read
   __syncthreads();
-  if (tid == 0) s_last = (atomicAdd(&p.counters[pair], 1u) == (unsigned)(nchunks - 1));
+  if (tid == 0) s_last = (count_chunk(&p.counters[pair]) == (unsigned)(nchunks - 1));
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
   if (tid == 0) p.counters[pair] = 0u;  // ready for the next call
   // The partials are staged in shared memory, a batch of chunks at a time;
   // thread j < g folds head j's maxima and sums and leaves one weight per
