@@ -10,6 +10,7 @@ libkin.so is missing or cannot be loaded, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -147,6 +148,10 @@ def load_library(path: str = LIB_PATH):
     return lib
 
 
+# a CUDA tensor at hand means that CUDA is initialised: the raw queries are enough
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
 def _dev(t: Optional[torch.Tensor], name: str, dtype=None, nullable=False, count: Optional[int] = None):
     """The device pointer of t after checking that it is a contiguous CUDA
     tensor on the current device, of an accepted dtype and, when count is
@@ -159,16 +164,16 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None, nullable=False, count
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != _current_device():
         raise ValueError(f"{name} is on {t.device}; the calls run on the current device "
                          f"cuda:{torch.cuda.current_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if dtype is not None and t.dtype is not dtype and (not isinstance(dtype, tuple) or t.dtype not in dtype):
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if count is not None and t.numel() < count:
         raise ValueError(f"{name} holds {t.numel()} elements; the dims need {count}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 class _Counts:
@@ -197,14 +202,24 @@ class _Counts:
         return None if per is None else int(n) * per
 
 
+@functools.lru_cache(maxsize=256)
+def _counts_of(*fields) -> _Counts:
+    return _Counts(kin_dims(*fields))
+
+
+def _counts(d: kin_dims) -> _Counts:
+    """The counts of these dims' values (kept: a decode loop asks for the same ones each step)."""
+    return _counts_of(d.batch, d.num_kv_heads, d.num_q_heads, d.head_dim, d.block_size, d.max_seq_len)
+
+
 def _status(dev_status):
-    return _dev(dev_status, "dev_status", torch.int32, nullable=True, count=1)
+    return None if dev_status is None else _dev(dev_status, "dev_status", torch.int32, nullable=True, count=1)
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return torch._C._cuda_getCurrentRawStream(_current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check(rc: int, where: str):
@@ -232,7 +247,7 @@ def alloc_workspace(dims: kin_dims, k_blocks: int, device="cuda") -> torch.Tenso
 
 
 def kin_block_means_build(dims, k_cache, seq_lens, block_means, dev_status=None, stream=None):
-    c = _Counts(dims)
+    c = _counts(dims)
     rc = load_library().kin_block_means_build(
         ctypes.byref(dims), _dev(k_cache, "k_cache", _BF16, count=c.cache),
         _dev(seq_lens, "seq_lens", torch.int32, count=c.lens),
@@ -242,7 +257,7 @@ def kin_block_means_build(dims, k_cache, seq_lens, block_means, dev_status=None,
 
 def kin_block_means_update(dims, k_cache, v_cache, block_means, seq_lens, k_new, v_new, n_new,
                            dev_status=None, stream=None):
-    c = _Counts(dims)
+    c = _counts(dims)
     new_rows = c.times(max(int(n_new), 0), c.bkd)
     rc = load_library().kin_block_means_update(
         ctypes.byref(dims), _dev(k_cache, "k_cache", _BF16, count=c.cache),
@@ -254,7 +269,7 @@ def kin_block_means_update(dims, k_cache, v_cache, block_means, seq_lens, k_new,
 
 def kin_block_topk_select(dims, q, block_means, seq_lens, k_blocks, sel_idx, sel_cnt, workspace,
                           dev_status=None, stream=None):
-    c = _Counts(dims)
+    c = _counts(dims)
     rc = load_library().kin_block_topk_select(
         ctypes.byref(dims), _dev(q, "q", _BF16, count=c.q), _dev(block_means, "block_means", torch.float32, count=c.means),
         _dev(seq_lens, "seq_lens", torch.int32, count=c.lens), int(k_blocks),
@@ -266,7 +281,7 @@ def kin_block_topk_select(dims, q, block_means, seq_lens, k_blocks, sel_idx, sel
 
 def kin_sparse_decode_attn(dims, q, k_cache, v_cache, seq_lens, sel_idx, sel_cnt, k_blocks,
                            softmax_scale, out, lse, workspace, dev_status=None, stream=None):
-    c = _Counts(dims)
+    c = _counts(dims)
     rc = load_library().kin_sparse_decode_attn(
         ctypes.byref(dims), _dev(q, "q", _BF16, count=c.q), _dev(k_cache, "k_cache", _BF16, count=c.cache),
         _dev(v_cache, "v_cache", _BF16, count=c.cache), _dev(seq_lens, "seq_lens", torch.int32, count=c.lens),
@@ -283,7 +298,7 @@ def kin_block_topk_select_noalloc(dims, q, block_means, seq_lens, k_blocks, sel_
     """kin_block_topk_select without a workspace, for callers that may not
     allocate device memory: the scratch lives in a fixed array inside
     libkin.so (see include/kin.h for its limit and its sharing rules)."""
-    c = _Counts(dims)
+    c = _counts(dims)
     rc = load_library().kin_block_topk_select_noalloc(
         ctypes.byref(dims), _dev(q, "q", _BF16, count=c.q), _dev(block_means, "block_means", torch.float32, count=c.means),
         _dev(seq_lens, "seq_lens", torch.int32, count=c.lens), int(k_blocks),
@@ -298,7 +313,7 @@ def kin_block_topk_select_noalloc(dims, q, block_means, seq_lens, k_blocks, sel_
 
 def kin_block_means_build_paged(dims, k_pages, block_table, seq_lens, block_means, dev_status=None,
                                 stream=None):
-    c = _Counts(dims)
+    c = _counts(dims)
     pages = int(k_pages.shape[0])
     rc = load_library().kin_block_means_build_paged(
         ctypes.byref(dims), _dev(k_pages, "k_pages", _BF16, count=c.times(pages, c.page)), pages,
@@ -310,7 +325,7 @@ def kin_block_means_build_paged(dims, k_pages, block_table, seq_lens, block_mean
 
 def kin_block_means_update_paged(dims, k_pages, v_pages, block_table, block_means, seq_lens, k_new, v_new,
                                  n_new, dev_status=None, stream=None):
-    c = _Counts(dims)
+    c = _counts(dims)
     pages = int(k_pages.shape[0])
     new_rows = c.times(max(int(n_new), 0), c.bkd)
     rc = load_library().kin_block_means_update_paged(
@@ -325,7 +340,7 @@ def kin_block_means_update_paged(dims, k_pages, v_pages, block_table, block_mean
 
 def kin_sparse_decode_attn_paged(dims, q, k_pages, v_pages, block_table, seq_lens, sel_idx, sel_cnt, k_blocks,
                                  softmax_scale, out, lse, workspace, dev_status=None, stream=None):
-    c = _Counts(dims)
+    c = _counts(dims)
     pages = int(k_pages.shape[0])
     rc = load_library().kin_sparse_decode_attn_paged(
         ctypes.byref(dims), _dev(q, "q", _BF16, count=c.q), _dev(k_pages, "k_pages", _BF16, count=c.times(pages, c.page)),
@@ -404,7 +419,7 @@ def _layout(rows, block_table, c: _Counts):
 def kin_block_means_build_ex(dims, k_rows, seq_lens, block_means, block_table=None, dev_status=None,
                              stream=None, per_page=False):
     """per_page: block_means is [num_pages, Hkv, D] (one mean per page; needs block_table)."""
-    c = _Counts(dims)
+    c = _counts(dims)
     pages, table, rows = _layout(k_rows, block_table, c)
     means, dtype = _means(block_means, c.times(pages, c.page_mean) if per_page else c.means, dims=dims,
                           pages=pages if per_page else None)
@@ -417,7 +432,7 @@ def kin_block_means_build_ex(dims, k_rows, seq_lens, block_means, block_table=No
 
 def kin_block_means_update_ex(dims, k_rows, v_rows, block_means, seq_lens, k_new, v_new, n_new,
                               block_table=None, dev_status=None, stream=None, per_page=False):
-    c = _Counts(dims)
+    c = _counts(dims)
     pages, table, rows = _layout(k_rows, block_table, c)
     means, dtype = _means(block_means, c.times(pages, c.page_mean) if per_page else c.means, dims=dims,
                           pages=pages if per_page else None)
@@ -433,7 +448,7 @@ def kin_block_means_update_ex(dims, k_rows, v_rows, block_means, seq_lens, k_new
 
 def kin_block_topk_select_ex(dims, q, block_means, seq_lens, k_blocks, sel_idx, sel_cnt, workspace,
                              dev_status=None, stream=None):
-    c = _Counts(dims)
+    c = _counts(dims)
     means, dtype = _means(block_means, c.means, dims=dims)
     rc = load_library().kin_block_topk_select_ex(
         ctypes.byref(dims), _dev(q, "q", _BF16, count=c.q), means, dtype,
@@ -459,7 +474,7 @@ def alloc_token_workspace(dims: kin_dims, k_tokens: int, device="cuda") -> torch
 
 def kin_token_topk_decode_attn(dims, q, k_cache, v_cache, seq_lens, k_tokens, softmax_scale, out, lse, workspace,
                                sel_tokens=None, dev_status=None, stream=None):
-    c = _Counts(dims)
+    c = _counts(dims)
     rc = load_library().kin_token_topk_decode_attn(
         ctypes.byref(dims), _dev(q, "q", _BF16, count=c.q), _dev(k_cache, "k_cache", _BF16, count=c.cache),
         _dev(v_cache, "v_cache", _BF16, count=c.cache), _dev(seq_lens, "seq_lens", torch.int32, count=c.lens),
@@ -476,7 +491,7 @@ def kin_block_topk_select_paged(dims, q, page_means, block_table, seq_lens, k_bl
     """The select over per-page block means [num_pages, Hkv, D] (fp32 or bf16),
     or a per-page dual buffer (uint8; num_pages then required), found through
     block_table: the shared-prompt layout (see include/kin.h)."""
-    c = _Counts(dims)
+    c = _counts(dims)
     if page_means is not None and page_means.dtype == torch.uint8:
         if num_pages is None:
             raise ValueError("page_means: a dual buffer needs num_pages")
@@ -518,17 +533,18 @@ class KvCache:
         pages, table, elements = 0, None, c.cache
         if self.block_table is not None:
             pages = int(self.k.shape[0])
-            table = _dev(self.block_table, name + ".block_table", torch.int32, count=c.table)
+            table = _dev(self.block_table, f"{name}.block_table", torch.int32, count=c.table)
             elements = c.times(pages, c.page)
-        codes = None if elements is None else elements // 2
-        rows = (torch.uint8, codes) if self.int4 else (_BF16, elements)
-        kv = kin_kv(KIN_KV_INT4 if self.int4 else KIN_KV_BF16, pages, table,
-                    _dev(self.k, name + ".k", rows[0], count=rows[1]), _dev(self.v, name + ".v", rows[0], count=rows[1]))
-        if self.int4:
-            scales = None if elements is None else elements // 32
-            kv.k_scales = _dev(self.k_scales, name + ".k_scales", _BF16, count=scales)
-            kv.v_scales = _dev(self.v_scales, name + ".v_scales", _BF16, count=scales)
-        return kv, pages
+        if self.k_scales is None:
+            return kin_kv(KIN_KV_BF16, pages, table, _dev(self.k, f"{name}.k", _BF16, count=elements),
+                          _dev(self.v, f"{name}.v", _BF16, count=elements), None, None), pages
+        codes = scales = None
+        if elements is not None:
+            codes, scales = elements >> 1, elements >> 5
+        return kin_kv(KIN_KV_INT4, pages, table, _dev(self.k, f"{name}.k", torch.uint8, count=codes),
+                      _dev(self.v, f"{name}.v", torch.uint8, count=codes),
+                      _dev(self.k_scales, f"{name}.k_scales", _BF16, count=scales),
+                      _dev(self.v_scales, f"{name}.v_scales", _BF16, count=scales)), pages
 
 
 def alloc_kv4(dims: kin_dims, num_pages: Optional[int] = None, block_table=None, device="cuda") -> KvCache:
@@ -557,7 +573,7 @@ def _kv_means(block_means, c: _Counts, dims, pages, per_page):
 def kin_kv4_store(dims, src: KvCache, dst: KvCache, seq_lens, block_means=None, dev_status=None, stream=None,
                   per_page=False):
     """A prefilled bf16 cache into a 4-bit one, with its block means."""
-    c = _Counts(dims)
+    c = _counts(dims)
     s, _ = src._struct(c, "src")
     d, pages = dst._struct(c, "dst")
     means, dtype = _kv_means(block_means, c, dims, pages, per_page)
@@ -570,7 +586,7 @@ def kin_kv4_store(dims, src: KvCache, dst: KvCache, seq_lens, block_means=None, 
 def kin_kv4_append(dims, kv: KvCache, block_means, seq_lens, new_lens, k_new, v_new, n_new, dev_status=None,
                    stream=None, per_page=False):
     """n_new tokens onto a 4-bit cache; new_lens may be seq_lens (in place)."""
-    c = _Counts(dims)
+    c = _counts(dims)
     d, pages = kv._struct(c, "kv")
     means, dtype = _kv_means(block_means, c, dims, pages, per_page)
     new_rows = c.times(max(int(n_new), 0), c.bkd)
@@ -584,7 +600,7 @@ def kin_kv4_append(dims, kv: KvCache, block_means, seq_lens, new_lens, k_new, v_
 def kin_kv4_load(dims, kv: KvCache, seq_lens, k_out, v_out, starts=None, n=None, dev_status=None, stream=None):
     """Rows of a 4-bit cache as bf16: n tokens a sequence from starts (0 when
     not given) into k_out / v_out [B, Hkv, n, D]; n defaults to k_out's."""
-    c = _Counts(dims)
+    c = _counts(dims)
     d, _ = kv._struct(c, "kv")
     n = int(k_out.shape[2]) if n is None else int(n)
     rows = c.times(max(n, 0), c.bkd)
@@ -612,7 +628,7 @@ def kin_kv_decode_attn(dims, q, kv: KvCache, seq_lens, sel_idx, sel_cnt, k_block
     """Decode attention over a bf16 or 4-bit cache; sel_idx and sel_cnt None
     with k_blocks 0 attend to every block; acc [B, Hkv, Lcap] fp32 takes the
     attention weights on top of what it holds."""
-    c = _Counts(dims)
+    c = _counts(dims)
     d, _ = kv._struct(c, "kv")
     k = int(k_blocks)
     acc_rows = None if c.cache is None else c.cache // dims.head_dim
@@ -642,7 +658,7 @@ def kin_kv_evict(dims, kv: KvCache, acc, seq_lens, n_keep, n_sink, n_recent, dst
                  workspace, block_means=None, sel_tokens=None, dev_status=None, stream=None, per_page=False):
     """The n_keep tokens of every (sequence, KV head) that stay (first n_sink,
     last n_recent, then by acc), moved in order to the cache dst."""
-    c, cd = _Counts(dims), _Counts(dst_dims)
+    c, cd = _counts(dims), _counts(dst_dims)
     s, _ = kv._struct(c, "kv")
     d, pages = dst._struct(cd, "dst")
     means, dtype = _kv_means(block_means, cd, dst_dims, pages, per_page)

@@ -652,21 +652,23 @@ kin_status means_layout(const kin_dims& d, const KvView& kv, const void* means, 
 // The two share a buffer, a page pool included.
 bool same_cache(const KvView& a, const KvView& b) { return a.k == b.k || a.v == b.v || a.k == b.v || a.v == b.k; }
 
-#ifndef KIN_KV4_CHUNK_TOKENS
-#define KIN_KV4_CHUNK_TOKENS 2048
-#endif
-
-// Kept blocks per attention CTA: 768 tokens (110 KB of 4-bit rows), fewer
-// when the grid would hold fewer than 2 CTAs per SM.
-int kv_chunk_blocks(const kin_dims& d, int k) {
-  const int by_tokens = KIN_KV4_CHUNK_TOKENS / d.block_size > 0 ? KIN_KV4_CHUNK_TOKENS / d.block_size : 1;
-  const int64_t by_grid = (int64_t)k * pairs_of(d) / (2 * kTargetSMs);
-  int ch = by_tokens;
-  if (by_grid < ch) ch = by_grid > 0 ? (int)by_grid : 1;
-  const int cap = kKvItemTiles / (d.block_size / kTileTokens);
-  if (ch > cap) ch = cap;
-  const int chunks = (k + ch - 1) / ch;  // chunks of even length
-  return (k + chunks - 1) / chunks;
+// How the attention cuts the (pair, kept block) slots into ranges, one per
+// CTA.  Selected blocks: as many even ranges as fill whole waves of
+// kKvCtasPerSm CTAs per SM, so that all CTAs end together.  Every block: the
+// lengths are only known on the device and a range may be empty, so ranges
+// hold at most 1024 tokens.  Never less than 128 tokens (a step of each
+// warp), nor more than a pair or kKvItemTiles tiles.
+int kv_range_blocks(const kin_dims& d, int k, bool dense) {
+  const int tpb = d.block_size / kTileTokens;
+  const int64_t slots = (int64_t)pairs_of(d) * k;
+  int64_t cap = (dense ? 64 : kKvItemTiles) / tpb;
+  if (cap > k) cap = k;
+  const int64_t wave = (int64_t)kTargetSMs * kKvCtasPerSm;
+  const int64_t waves = (slots + wave * cap - 1) / (wave * cap);
+  int64_t per = (slots + wave * waves - 1) / (wave * waves);
+  const int least = (8 + tpb - 1) / tpb;
+  if (per < least) per = least;
+  return (int)(per < cap ? per : cap);
 }
 
 // The slots of the kept blocks of a pair: at most k_blocks, at most all.
@@ -674,6 +676,9 @@ int kv_slots(const kin_dims& d, int k_blocks) {
   const int nb = nbcap_of(d);
   return k_blocks == 0 || k_blocks > nb ? nb : k_blocks;
 }
+
+// CTAs whose ranges a pair's slots may meet.
+int kv_max_chunks(int k, int per) { return (k + per - 2) / per + 1; }
 
 struct KvWs {
   size_t counters, partials, z, lse2, total;
@@ -689,8 +694,7 @@ KvWs kv_ws_layout(const kin_dims& d, int k_blocks, bool acc) {
   w.counters = 0;
   off = k_blocks >= 2 ? ws_layout(d, k_blocks).total : align_up(pairs * sizeof(uint32_t));
   w.partials = off;
-  const int ch = kv_chunk_blocks(d, k);
-  off = align_up(off + pairs * (size_t)((k + ch - 1) / ch) * g * kPartStride * sizeof(float));
+  off = align_up(off + pairs * (size_t)kv_max_chunks(k, kv_range_blocks(d, k, k_blocks == 0)) * g * kPartStride * sizeof(float));
   w.z = off;
   if (acc) off = align_up(off + pairs * (size_t)k * d.block_size * g * sizeof(float));
   w.lse2 = off;
@@ -829,8 +833,9 @@ KIN_EXPORT kin_status kin_kv_decode_attn(const kin_dims* dims, const void* q, co
   p.bs = dims->block_size;
   p.k_row = k_blocks;
   p.k = kv_slots(*dims, k_blocks);
-  p.chunk_blocks = kv_chunk_blocks(*dims, p.k);
-  p.max_chunks = (p.k + p.chunk_blocks - 1) / p.chunk_blocks;
+  p.slots = pairs_of(*dims) * p.k;
+  p.per = kv_range_blocks(*dims, p.k, k_blocks == 0);
+  p.max_chunks = kv_max_chunks(p.k, p.per);
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)kHeadDim);
   p.scale_log2 = scale * 1.4426950408889634f;
   return from_cuda(launch_kv_attn(p, static_cast<cudaStream_t>(stream)));

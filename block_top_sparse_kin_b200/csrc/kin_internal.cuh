@@ -326,7 +326,11 @@ struct TokenParams {
 // A cache as kin_kv describes it.  INT4 rows: kCodeBytes bytes of codes and
 // kGroups bf16 scales, one per kGroupDim channels (see kin.h).
 constexpr int kGroupDim = 32;
-constexpr int kKvItemTiles = 128;  // attention tiles per work item (32 per warp, one per lane)
+#ifndef KIN_KV_CTAS_PER_SM
+#define KIN_KV_CTAS_PER_SM 3
+#endif
+constexpr int kKvCtasPerSm = KIN_KV_CTAS_PER_SM;  // resident CTAs of the attention
+constexpr int kKvItemTiles = 256;  // attention tiles per CTA and pair (64 per warp, two per lane)
 constexpr int kGroups = kHeadDim / kGroupDim;
 constexpr int kCodeBytes = kHeadDim / 2;
 
@@ -396,7 +400,9 @@ struct KvAttnParams {
   int32_t* dev_status;
   int B, Hkv, Hq, g, bs;
   int k, k_row;            // kept blocks a pair may have; stride of sel_idx
-  int chunk_blocks, max_chunks;
+  int slots;               // pairs x k
+  int per;                 // slots of a CTA
+  int max_chunks;          // CTAs that a pair's slots may meet
   float scale_log2;
 };
 

@@ -25,8 +25,8 @@ namespace {
 
 #define kNegInf (-__int_as_float(0x7f800000))
 
-#ifndef KIN_KV4_CTAS_PER_SM
-#define KIN_KV4_CTAS_PER_SM 4
+#ifndef KIN_KV4_STAGES
+#define KIN_KV4_STAGES 3
 #endif
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
@@ -35,14 +35,17 @@ constexpr int kHalfBox = 16 * 64 * 2;
 
 template <bool kInt4>
 struct Ring {
+  // tiles of 16 tokens that a warp takes at a step
+  static constexpr int kStep = kInt4 ? 2 : 1;
   // bf16: K0 K1 V0 V1 half tiles of 16 rows x 64 channels.  4 bit: 16 rows of
   // 64 bytes of key codes, of value codes, then 16 x 4 scales of each.
-  static constexpr int kStageBytes = kInt4 ? 2 * 16 * kCodeBytes + 2 * 16 * kGroups * 2 : 4 * kHalfBox;
-  static constexpr int kStages = kInt4 ? 4 : 2;
-  // 4 bit, per warp behind the ring: the tile's key scales as fp32 [16][4] and
-  // its value scales as fp16 pairs [8 token pairs][4]
+  static constexpr int kTileBytes = kInt4 ? 2 * 16 * kCodeBytes + 2 * 16 * kGroups * 2 : 4 * kHalfBox;
+  static constexpr int kStageBytes = kStep * kTileBytes;
+  static constexpr int kStages = kInt4 ? KIN_KV4_STAGES : 2;
+  // 4 bit, per warp and tile behind the ring: the tile's key scales as fp32
+  // [16][4] and its value scales as fp16 pairs [8 token pairs][4]
   static constexpr int kScaleBytes = kInt4 ? 256 + 128 : 0;
-  static constexpr int kPipe = kWarps * (kStages * kStageBytes + kScaleBytes);
+  static constexpr int kPipe = kWarps * (kStages * kStageBytes + kStep * kScaleBytes);
   static constexpr int kComb = kWarps * kMaxGroup * kRowPad * 4;
   static constexpr int kSmem = (kPipe > kComb ? kPipe : kComb) + 1024;
 };
@@ -64,16 +67,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
-}
-
-// D = A B + C with C left as it is
-__device__ __forceinline__ void mma_f16_from(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
-      "{%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -157,12 +150,17 @@ struct Acc {
   float m[2], thr[2], r[2], l[2];
 };
 
-// The tile's weights p from its raw logits s (rows tq, tq + 8; heads ta,
+// The weights p of N tiles from their raw logits s (rows tq, tq + 8; heads ta,
 // ta + 1; -inf where there is no token); sl2: base-2 scale of the two heads.
-__device__ __forceinline__ void weigh(Acc& a, const float (&s)[4], const float (&sl2)[2], float (&p)[4]) {
-  const float x0 = fmaxf(s[0], s[2]), x1 = fmaxf(s[1], s[3]);
-  if (__any_sync(0xffffffffu, x0 > a.thr[0] || x1 > a.thr[1])) {
-    float x[2] = {x0, x1};
+template <int N>
+__device__ __forceinline__ void weigh(Acc& a, const float (&s)[N][4], const float (&sl2)[2], float (&p)[N][4]) {
+  float x[2] = {fmaxf(s[0][0], s[0][2]), fmaxf(s[0][1], s[0][3])};
+#pragma unroll
+  for (int h = 1; h < N; ++h) {
+    x[0] = fmaxf(x[0], fmaxf(s[h][0], s[h][2]));
+    x[1] = fmaxf(x[1], fmaxf(s[h][1], s[h][3]));
+  }
+  if (__any_sync(0xffffffffu, x[0] > a.thr[0] || x[1] > a.thr[1])) {
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
       x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], off));
@@ -186,18 +184,21 @@ __device__ __forceinline__ void weigh(Acc& a, const float (&s)[4], const float (
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    p[i] = exp2_approx(fmaf(s[i], sl2[i & 1], -a.r[i & 1]));
-    a.l[i & 1] += p[i];
+  for (int h = 0; h < N; ++h) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[h][i] = exp2_approx(fmaf(s[h][i], sl2[i & 1], -a.r[i & 1]));
+      a.l[i & 1] += p[h][i];
+    }
   }
 }
 
 }  // namespace
 
 template <bool kInt4, bool kAcc>
-__global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_attn_kernel(KvAttnParams p) {
+__global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnParams p) {
   using R = Ring<kInt4>;
-  constexpr int kStages = R::kStages;
+  constexpr int kStages = R::kStages, kStep = R::kStep;
   extern __shared__ uint8_t smem_raw[];
   __shared__ float s_m[kWarps][kMaxGroup], s_l[kWarps][kMaxGroup];
   __shared__ int s_last;
@@ -211,29 +212,42 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_
   pdl_wait();  // the selection comes from the select kernels
   pdl_trigger_early();
   const int tpb = bs / kTileTokens;
-  const int64_t pair = blockIdx.x / p.max_chunks;
-  const int chunk = (int)(blockIdx.x - pair * p.max_chunks);
-  // lane l's tile of this warp (tile warp + W l of the chunk): its block index
-  // is requested before the length and count, whose round trip it would follow
-  int blk = -1;
-  {
-    const int t = warp + kWarps * lane;
-    const int j = chunk * p.chunk_blocks + t / tpb;
-    if (t < p.chunk_blocks * tpb && j < p.k) blk = p.sel_idx ? __ldg(p.sel_idx + pair * p.k_row + j) : j;
+  const int n = lane >> 2, c = lane & 3;
+  const int tq = lane >> 2, ta = 2 * c;
+
+  // This CTA's range of the (pair, kept block) slots, cut at pair boundaries:
+  // blocks [j0, j1) of one pair at a time.
+  const int hi_slot = min((int)(blockIdx.x + 1) * p.per, p.slots);
+  for (int at = blockIdx.x * p.per; at < hi_slot;) {
+  const int pair = at / p.k, j0 = at - pair * p.k;
+  const int j1 = min(p.k, hi_slot - pair * p.k);
+  at = (pair + 1) * p.k;
+  // lane l's tiles l and l + 32 of this warp (steps warp, warp + W, .. of the
+  // range, kStep tiles each): their block indices are requested before the
+  // length and count, whose round trip they would follow
+  int my_tile[2], blk[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int i = lane + 32 * r;
+    my_tile[r] = (warp + kWarps * (i / kStep)) * kStep + i % kStep;
+    const int j = j0 + my_tile[r] / tpb;
+    blk[r] = j;
+    if (p.sel_idx) blk[r] = j < j1 ? __ldg(p.sel_idx + (int64_t)pair * p.k_row + j) : -1;
   }
-  const int b = (int)(pair / p.Hkv), h = (int)(pair - (int64_t)b * p.Hkv);
+  const int b = pair / p.Hkv, h = pair - b * p.Hkv;
+  const int64_t qh0 = (int64_t)b * p.Hq + (int64_t)h * g;
+  const __nv_bfloat16* qrow = p.q + (qh0 + (n < g ? n : 0)) * kHeadDim;
+  uint4 qw[4];  // 4 bit
+#pragma unroll
+  for (int G = 0; G < 4 && kInt4; ++G) qw[G] = __ldg(reinterpret_cast<const uint4*>(qrow + 32 * G + 8 * c));
   const int L = __ldg(p.seq_lens + b);
   const bool bad_len = L < 1 || L > Lcap;
   const int nb = bad_len ? 0 : (L + bs - 1) / bs;
   int cnt = p.sel_idx ? __ldg(p.sel_cnt + pair) : nb;
   if (bad_len) cnt = 0;
   if (cnt > p.k) cnt = p.k;
-  const int nchunks = cnt > 0 ? (cnt + p.chunk_blocks - 1) / p.chunk_blocks : 0;
-  const int j0 = chunk * p.chunk_blocks;
-  const int ntiles = chunk < nchunks ? (min(j0 + p.chunk_blocks, cnt) - j0) * tpb : 0;
-  const int64_t qh0 = (int64_t)b * p.Hq + (int64_t)h * g;
   if (cnt <= 0) {  // nothing to attend to: out = 0, lse = -inf
-    if (chunk == 0) {
+    if (j0 == 0) {
       for (int j = 0; j < g; ++j) p.out[(qh0 + j) * kHeadDim + tid] = __float2bfloat16_rn(0.f);
       if (tid < g) {
         if (p.lse) p.lse[qh0 + tid] = kNegInf;
@@ -241,32 +255,119 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_
       }
       if (bad_len && tid == 0) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
     }
-    return;
+    continue;
   }
-  if (ntiles == 0) return;
+  const int ntiles = (min(j1, cnt) - j0) * tpb;
+  if (ntiles <= 0) continue;
+  // the pair's ranges that hold a kept block, and this one's place among them
+  const int first_cta = pair * p.k / p.per;
+  const int nchunks = (pair * p.k + cnt - 1) / p.per - first_cta + 1, chunk = blockIdx.x - first_cta;
 
-  // this warp's tiles t = warp + W n; lane n holds tile n's first row (a cache
-  // of 2^31 rows is larger than the memory) and its valid rows; kPartial marks
-  // a tile of less than 16
-  constexpr uint32_t kPartial = 0x80000000u;
-  const int n_w = warp < ntiles ? (ntiles - 1 - warp) / kWarps + 1 : 0;
-  uint32_t my_row = kPartial;
-  int my_nvalid = 0;
-  if (lane < n_w) {
-    const int t = warp + kWarps * lane;
-    const int tok = blk * bs + (t % tpb) * kTileTokens;
-    int64_t row = -1;
-    if (blk >= 0 && blk < nb && tok < L) row = kv_row(p.kv.pages, b, h, p.Hkv, Lcap, bs, tok);
-    if (blk < 0 || blk >= nb || (tok < L && row < 0)) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
-    my_nvalid = row < 0 ? 0 : min(kTileTokens, L - tok);
-    my_row = (row < 0 ? 0u : (uint32_t)row) | (my_nvalid < kTileTokens ? kPartial : 0u);
+  // lane n holds its tiles' first rows (a cache of 2^31 rows is larger than
+  // the memory) and valid rows; bit n of `partial` marks a tile of less than 16
+  const int n_w = warp * kStep < ntiles ? (ntiles - 1 - warp * kStep) / (kWarps * kStep) + 1 : 0;  // steps
+  uint32_t my_row[2] = {0u, 0u}, partial[2];
+  int my_nvalid[2] = {0, 0};
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    if (my_tile[r] < ntiles) {
+      const int tok = blk[r] * bs + (my_tile[r] % tpb) * kTileTokens;
+      const bool there = blk[r] >= 0 && blk[r] < nb;
+      int64_t row = -1;
+      if (there && tok < L) row = kv_row(p.kv.pages, b, h, p.Hkv, Lcap, bs, tok);
+      if (!there || (tok < L && row < 0)) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
+      my_nvalid[r] = row < 0 ? 0 : min(kTileTokens, L - tok);
+      my_row[r] = row < 0 ? 0u : (uint32_t)row;
+    }
+    partial[r] = __ballot_sync(0xffffffffu, my_nvalid[r] < kTileTokens);
   }
+  auto tile_row = [&](int i) { return __shfl_sync(0xffffffffu, i < 32 ? my_row[0] : my_row[1], i & 31); };
+  auto tile_valid = [&](int i) { return __shfl_sync(0xffffffffu, i < 32 ? my_nvalid[0] : my_nvalid[1], i & 31); };
+  auto tile_partial = [&](int i) { return (i < 32 ? partial[0] : partial[1]) >> (i & 31); };
+
+  const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * (kStages * R::kStageBytes + kStep * R::kScaleBytes));
+  const uint32_t scales = ring + kStages * R::kStageBytes;
+  // 4 bit: 64 pieces of 16 bytes of key codes and of value codes, 8 bytes of
+  // scales for each row.  Key row i of the tile holds token (i & 8) + 4 (i & 1)
+  // + (i & 7) / 2, so that the tile's k slots 2c, 2c + 1 of the second product
+  // are tokens c, c + 4 (and 8 + c, 12 + c); the value rows stay in token
+  // order, their pieces 2 and 3 swapped with 0 and 1 in every second pair of
+  // rows, which keeps their 8-byte reads free of bank conflicts.
+  const int it = lane >> 2, icol = lane & 3;
+  const uint32_t k_dst = ring + (((it & 3) << 1) | (it >> 2)) * 64 + icol * 16;
+  const uint32_t v_dst = ring + 1024 + it * 64 + ((icol ^ (it & 2)) << 4);
+  const uint32_t s_dst = ring + 2048 + lane * 8;
+  const uint8_t* k_src = p.kv.k + lane * 16;
+  const uint8_t* v_src = p.kv.v + lane * 16;
+  const uint16_t* s_src = (lane < 16 ? p.kv.ks : p.kv.vs) + (lane & 15) * kGroups;
+  auto issue_tile = [&](int nt, uint32_t slot) {  // slot: byte offset of the tile's place in the ring
+    const uint32_t row = tile_row(nt);
+    if (!(tile_partial(nt) & 1u)) {
+      if constexpr (kInt4) {
+        const uint8_t* ks = k_src + (uint64_t)row * kCodeBytes;
+        const uint8_t* vs = v_src + (uint64_t)row * kCodeBytes;
+        cp_async16(k_dst + slot, ks, 16u);
+        cp_async16(k_dst + slot + 512, ks + 512, 16u);
+        cp_async16(v_dst + slot, vs, 16u);
+        cp_async16(v_dst + slot + 512, vs + 512, 16u);
+        cp_async8(s_dst + slot, s_src + (uint64_t)row * kGroups, 8u);
+      } else {
+        const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.kv.k) + (uint64_t)row * kHeadDim;
+        const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.kv.v) + (uint64_t)row * kHeadDim;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int piece = lane + 32 * i;
+          const int r = piece >> 4, cc = piece & 15;
+          const uint32_t off = ring + slot + (uint32_t)((cc >> 3) * kHalfBox + r * 128 + (((cc & 7) ^ (r & 7)) << 4));
+          cp_async16(off, k + piece * 8, 16u);
+          cp_async16(off + 2 * kHalfBox, v + piece * 8, 16u);
+        }
+      }
+    } else {  // rows behind the length: zeros, nothing read (the address stays on a valid row)
+      const int nv = tile_valid(nt);
+      if constexpr (kInt4) {
+        // a tile without any row: its scales become zeros, its codes may be
+        // anything (every nibble is a finite number and its weight is zero)
+        if (nv > 0) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int t = it + 8 * i;
+            const int64_t from = (int64_t)row * kCodeBytes + (t < nv ? 512 * i : -it * 64);
+            cp_async16(k_dst + slot + 512 * i, k_src + from, t < nv ? 16u : 0u);
+            cp_async16(v_dst + slot + 512 * i, v_src + from, t < nv ? 16u : 0u);
+          }
+        }
+        const int t = lane & 15;
+        cp_async8(s_dst + slot, s_src + (int64_t)row * kGroups - (t < nv ? 0 : t * kGroups), t < nv ? 8u : 0u);
+      } else if (nv > 0) {
+        const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.kv.k) + (uint64_t)row * kHeadDim;
+        const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.kv.v) + (uint64_t)row * kHeadDim;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int piece = lane + 32 * i;
+          const int r = piece >> 4, cc = piece & 15;
+          const uint32_t off = ring + slot + (uint32_t)((cc >> 3) * kHalfBox + r * 128 + (((cc & 7) ^ (r & 7)) << 4));
+          const int src = (r < nv ? r : 0) * kHeadDim + cc * 8;
+          const uint32_t bytes = r < nv ? 16u : 0u;
+          cp_async16(off, k + src, bytes);
+          cp_async16(off + 2 * kHalfBox, v + src, bytes);
+        }
+      }
+    }
+  };
+  auto issue = [&](int st, uint32_t slot) {
+    if (st < n_w) {
+#pragma unroll
+      for (int h = 0; h < kStep; ++h) issue_tile(st * kStep + h, slot + h * R::kTileBytes);
+    }
+    cp_async_commit();  // one group per step, empty or not
+  };
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) issue(i, i * R::kStageBytes);
 
   // Q fragments (B operand): head n = lane / 4.  sl2: the base-2 scale of the
   // raw logits of heads ta and ta + 1.
   uint32_t qf[8][2];
-  const int n = lane >> 2, c = lane & 3;
-  const int tq = lane >> 2, ta = 2 * c;
   float sl2[2] = {p.scale_log2, p.scale_log2};
   // 4 bit: key nibbles enter the first product as the fp16 numbers n 2^-24
   // (bits 0..3 of a half) and n 2^-20 (bits 4..7): one AND for two, no
@@ -274,15 +375,16 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_
   // largest magnitude in [2^14, 2^15): its 8 bits are kept exactly down to
   // 2^-31 of that, and what is lost below is under fp32's own rounding.  The
   // channels met by n 2^-20 are scaled by 2^-4 more.  A nibble is c + 8: each
-  // group's sum starts at -8 times its sum of q, from a product with ones.
-  float qs[4][4];
-  const __nv_bfloat16* qrow = p.q + (qh0 + (n < g ? n : 0)) * kHeadDim;
+  // group's sum is short of -8 times its sum of q, and the logit of -8 sum_g
+  // ks_g sum q_g: one product of the scales with that sum in three bf16 parts
+  // (24 bits), k slots 0..3 the high parts of groups 0..3, 4..7 the middle,
+  // 8..11 the low ones.
+  uint32_t off_b[2] = {0u, 0u};
   if constexpr (kInt4) {
-    uint4 w[4];
+    uint4(&w)[4] = qw;
     uint32_t mx = 0;
 #pragma unroll
     for (int G = 0; G < 4; ++G) {
-      w[G] = __ldg(reinterpret_cast<const uint4*>(qrow + 32 * G + 8 * c));
       if (n >= g) w[G] = make_uint4(0u, 0u, 0u, 0u);
       mx = max_u16x2(mx, max_u16x2(max_u16x2(w[G].x & 0x7FFF7FFFu, w[G].y & 0x7FFF7FFFu),
                                    max_u16x2(w[G].z & 0x7FFF7FFFu, w[G].w & 0x7FFF7FFFu)));
@@ -305,13 +407,22 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_
         const float fi = (i & 1) ? f4 : f;
         qf[2 * G + (i >> 1)][i & 1] = pack_f16x2(lo_f(v[i]) * fi, hi_f(v[i]) * fi);
       }
-      // ones for the first channels of a step, 2^4 for the scaled ones
-      qs[G][0] = qs[G][1] = qs[G][2] = qs[G][3] = 0.f;
-      mma_f16_16816(qs[G], 0x3C003C00u, 0x3C003C00u, 0x4C004C00u, 0x4C004C00u, qf[2 * G][0], qf[2 * G][1]);
-      mma_f16_16816(qs[G], 0x3C003C00u, 0x3C003C00u, 0x4C004C00u, 0x4C004C00u, qf[2 * G + 1][0], qf[2 * G + 1][1]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) qs[G][i] *= -0x1p-21f;  // -8 * 2^-24
     }
+    float part[4];
+#pragma unroll
+    for (int G = 0; G < 4; ++G) {
+      float sum = lo_f(w[G].x) * f + hi_f(w[G].x) * f + lo_f(w[G].y) * f + hi_f(w[G].y) * f + lo_f(w[G].z) * f +
+                  hi_f(w[G].z) * f + lo_f(w[G].w) * f + hi_f(w[G].w) * f;
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      part[G] = sum * -0x1p-21f;  // -8 * 2^-24
+    }
+    const float x0 = (c & 1) ? part[2] : part[0], x1 = (c & 1) ? part[3] : part[1];
+    const uint32_t hi = pack_bf16x2(x0, x1);
+    const float m0 = x0 - lo_f(hi), m1 = x1 - hi_f(hi);
+    const uint32_t mid = pack_bf16x2(m0, m1);
+    off_b[0] = c < 2 ? hi : mid;
+    off_b[1] = c < 2 ? pack_bf16x2(m0 - lo_f(mid), m1 - hi_f(mid)) : 0u;
   } else {
     const uint32_t* q32 = reinterpret_cast<const uint32_t*>(qrow);
 #pragma unroll
@@ -320,79 +431,6 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_
       qf[kk][1] = n < g ? __ldg(q32 + kk * 8 + 4 + c) : 0u;
     }
   }
-
-  const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * (kStages * R::kStageBytes + R::kScaleBytes));
-  const uint32_t scales = ring + kStages * R::kStageBytes;
-  // 4 bit: 64 pieces of 16 bytes of key codes and of value codes, 8 bytes of
-  // scales for each row.  Key row i of the tile holds token (i & 8) + 4 (i & 1)
-  // + (i & 7) / 2, so that the tile's k slots 2c, 2c + 1 of the second product
-  // are tokens c, c + 4 (and 8 + c, 12 + c); the value rows stay in token
-  // order, their pieces 2 and 3 swapped with 0 and 1 in every second pair of
-  // rows, which keeps their 8-byte reads free of bank conflicts.
-  const int it = lane >> 2, icol = lane & 3;
-  const uint32_t k_dst = ring + (((it & 3) << 1) | (it >> 2)) * 64 + icol * 16;
-  const uint32_t v_dst = ring + 1024 + it * 64 + ((icol ^ (it & 2)) << 4);
-  const uint32_t s_dst = ring + 2048 + lane * 8;
-  const uint8_t* k_src = p.kv.k + lane * 16;
-  const uint8_t* v_src = p.kv.v + lane * 16;
-  const uint16_t* s_src = (lane < 16 ? p.kv.ks : p.kv.vs) + (lane & 15) * kGroups;
-  auto issue = [&](int nt, uint32_t slot) {  // slot: byte offset of the ring slot
-    const uint32_t row = nt < n_w ? __shfl_sync(0xffffffffu, my_row, nt & 31) : kPartial;
-    if (row < kPartial) {
-      if constexpr (kInt4) {
-        const uint8_t* ks = k_src + (uint64_t)row * kCodeBytes;
-        const uint8_t* vs = v_src + (uint64_t)row * kCodeBytes;
-        cp_async16(k_dst + slot, ks, 16u);
-        cp_async16(k_dst + slot + 512, ks + 512, 16u);
-        cp_async16(v_dst + slot, vs, 16u);
-        cp_async16(v_dst + slot + 512, vs + 512, 16u);
-        cp_async8(s_dst + slot, s_src + (uint64_t)row * kGroups, 8u);
-      } else {
-        const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.kv.k) + (uint64_t)row * kHeadDim;
-        const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.kv.v) + (uint64_t)row * kHeadDim;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int piece = lane + 32 * i;
-          const int r = piece >> 4, cc = piece & 15;
-          const uint32_t off = ring + slot + (uint32_t)((cc >> 3) * kHalfBox + r * 128 + (((cc & 7) ^ (r & 7)) << 4));
-          cp_async16(off, k + piece * 8, 16u);
-          cp_async16(off + 2 * kHalfBox, v + piece * 8, 16u);
-        }
-      }
-    } else if (nt < n_w) {  // rows behind the length: zeros, nothing read (the address stays on a valid row)
-      const int nv = __shfl_sync(0xffffffffu, my_nvalid, nt & 31);
-      const uint64_t r0 = row & ~kPartial;
-      if (nv > 0) {
-        if constexpr (kInt4) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int t = it + 8 * i;
-            const int64_t from = (int64_t)r0 * kCodeBytes + (t < nv ? 512 * i : -it * 64);
-            cp_async16(k_dst + slot + 512 * i, k_src + from, t < nv ? 16u : 0u);
-            cp_async16(v_dst + slot + 512 * i, v_src + from, t < nv ? 16u : 0u);
-          }
-          const int t = lane & 15;
-          cp_async8(s_dst + slot, s_src + (int64_t)r0 * kGroups - (t < nv ? 0 : t * kGroups), t < nv ? 8u : 0u);
-        } else {
-          const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.kv.k) + r0 * kHeadDim;
-          const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.kv.v) + r0 * kHeadDim;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int piece = lane + 32 * i;
-            const int r = piece >> 4, cc = piece & 15;
-            const uint32_t off = ring + slot + (uint32_t)((cc >> 3) * kHalfBox + r * 128 + (((cc & 7) ^ (r & 7)) << 4));
-            const int src = (r < nv ? r : 0) * kHeadDim + cc * 8;
-            const uint32_t bytes = r < nv ? 16u : 0u;
-            cp_async16(off, k + src, bytes);
-            cp_async16(off + 2 * kHalfBox, v + src, bytes);
-          }
-        }
-      }
-    }
-    cp_async_commit();  // one group per tile, empty or not
-  };
-#pragma unroll
-  for (int i = 0; i < kStages; ++i) issue(i, i * R::kStageBytes);
 
   Acc a;
 #pragma unroll
@@ -409,73 +447,104 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_
   bool v_nan = false;
   uint32_t slot = 0;
 
-  for (int nt = 0; nt < n_w; ++nt) {
+  for (int st = 0; st < n_w; ++st) {
     cp_async_wait<kStages - 1>();
     __syncwarp();
-    int nvalid = kTileTokens;
-    if (__shfl_sync(0xffffffffu, my_row, nt & 31) & kPartial) nvalid = __shfl_sync(0xffffffffu, my_nvalid, nt & 31);
-    if (nvalid > 0) {
+    int nv[kStep];
+    bool some = true;
+#pragma unroll
+    for (int h = 0; h < kStep; ++h) nv[h] = kTileTokens;
+    const uint32_t part = tile_partial(st * kStep) & ((1u << kStep) - 1u);
+    if (part) {
+      some = false;
+#pragma unroll
+      for (int h = 0; h < kStep; ++h) {
+        nv[h] = tile_valid(st * kStep + h);
+        some |= nv[h] > 0;
+      }
+    }
+    if (some) {
       const uint32_t base = ring + slot;
-      float s[4], pr[4];
-      int t0, t1;  // the tokens of this lane's logits
+      float s[kStep][4], pr[kStep][4];
+      int t0, t1;  // the tokens, in a tile, of this lane's logits
       if constexpr (kInt4) {
-        const uint4 wa = lds128(base + lane * 16), wb = lds128(base + 512 + lane * 16);
-        {
-          // the tile's scales, each unpacked once for the warp: lane l the key
-          // scales of token l / 2, groups 2 (l % 2) and the next; and group
-          // l % 4's value scales of token pair l / 4 (tokens tp, tp + 4)
-          const uint32_t kw = lds32(base + 2048 + lane * 4);
-          const int tp = (it & 3) + 8 * (it >> 2);
-          float v0 = __uint_as_float(lds16(base + 2176 + tp * 8 + icol * 2) << 16);
-          float v1 = __uint_as_float(lds16(base + 2176 + tp * 8 + 32 + icol * 2) << 16);
-          sts64(scales + lane * 8, lo_f(kw), hi_f(kw));
-          float vn = __uint_as_float(vn_bits);
-          if (__any_sync(0xffffffffu, !(v0 < vn) || !(v1 < vn))) {
-            // a scale that is not finite makes its group NaN whatever its
-            // weight: noted here, and kept out of the products
-            v_nan |= !(v0 < 0x1p127f) || !(v1 < 0x1p127f);
-            if (!(v0 < 0x1p127f)) v0 = 0.f;
-            if (!(v1 < 0x1p127f)) v1 = 0.f;
-            // a larger one moves the group's sums to its power of two
-            uint32_t mb = __float_as_uint(fmaxf(v0, v1));
+        // the scales, each unpacked once for the warp: lane l the key scales of
+        // token l / 2, groups 2 (l % 2) and the next; and group l % 4's value
+        // scales of token pair l / 4 (tokens tp, tp + 4)
+        const int tp = (it & 3) + 8 * (it >> 2);
+        float v[kStep][2];
+        const float vn = __uint_as_float(vn_bits);
+        bool high = false;
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, off));
-            const uint32_t e = mb >= vn_bits ? min((mb >> 23) + 1u, 253u) : vn_bits >> 23;
-            inv_vn = __uint_as_float((254u - e) << 23);
-            const float down = vn * inv_vn;
-            vn_bits = e << 23;
-            const float mine = __shfl_sync(0xffffffffu, down, tq & 3);
+        for (int h = 0; h < kStep; ++h) {
+          const uint32_t kw = lds32(base + h * R::kTileBytes + 2048 + lane * 4);
+          v[h][0] = __uint_as_float(lds16(base + h * R::kTileBytes + 2176 + tp * 8 + icol * 2) << 16);
+          v[h][1] = __uint_as_float(lds16(base + h * R::kTileBytes + 2176 + tp * 8 + 32 + icol * 2) << 16);
+          sts64(scales + h * R::kScaleBytes + lane * 8, lo_f(kw), hi_f(kw));
+          high |= !(v[h][0] < vn) || !(v[h][1] < vn);
+        }
+        if (__any_sync(0xffffffffu, high)) {
+          // a scale that is not finite makes its group NaN whatever its
+          // weight: noted here, and kept out of the products
+          uint32_t mb = 0u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a.sums[i] *= mine;
+          for (int h = 0; h < kStep; ++h) {
 #pragma unroll
-            for (int dm = 0; dm < 8; ++dm) {
-              const float dg = __shfl_sync(0xffffffffu, down, dm >> 1);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) a.o[dm][i] *= dg;
+            for (int i = 0; i < 2; ++i) {
+              if (!(v[h][i] < 0x1p127f)) {
+                v_nan = true;
+                v[h][i] = 0.f;
+              }
+              if (v[h][i] > 0.f) mb = max(mb, __float_as_uint(v[h][i]));
             }
           }
-          sts32(scales + 256 + lane * 4, pack_f16x2(v0 * inv_vn, v1 * inv_vn));
+          // a larger one moves the group's sums to its power of two
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, off));
+          const uint32_t e = mb >= vn_bits ? min((mb >> 23) + 1u, 253u) : vn_bits >> 23;
+          inv_vn = __uint_as_float((254u - e) << 23);
+          const float down = vn * inv_vn;
+          vn_bits = e << 23;
+          const float mine = __shfl_sync(0xffffffffu, down, tq & 3);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a.sums[i] *= mine;
+#pragma unroll
+          for (int dm = 0; dm < 8; ++dm) {
+            const float dg = __shfl_sync(0xffffffffu, down, dm >> 1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a.o[dm][i] *= dg;
+          }
         }
+#pragma unroll
+        for (int h = 0; h < kStep; ++h)
+          sts32(scales + h * R::kScaleBytes + 256 + lane * 4, pack_f16x2(v[h][0] * inv_vn, v[h][1] * inv_vn));
         __syncwarp();
-        const uint32_t ka[4] = {wa.x, wa.y, wa.z, wa.w}, kb[4] = {wb.x, wb.y, wb.z, wb.w};
         t0 = ((tq & 1) << 2) | (tq >> 1);
         t1 = t0 + 8;
-        const uint4 sa = lds128(scales + t0 * 16), sb = lds128(scales + t1 * 16);
-        const float fa4[4] = {__uint_as_float(sa.x), __uint_as_float(sa.y), __uint_as_float(sa.z), __uint_as_float(sa.w)};
-        const float fb4[4] = {__uint_as_float(sb.x), __uint_as_float(sb.y), __uint_as_float(sb.z), __uint_as_float(sb.w)};
 #pragma unroll
-        for (int G = 0; G < 4; ++G) {
-          float d[4];
-          const uint32_t ha = ka[G] >> 8, hb = kb[G] >> 8;
-          mma_f16_from(d, qs[G], ka[G] & 0x000F000Fu, kb[G] & 0x000F000Fu, ka[G] & 0x00F000F0u, kb[G] & 0x00F000F0u,
-                       qf[2 * G][0], qf[2 * G][1]);
-          mma_f16_16816(d, ha & 0x000F000Fu, hb & 0x000F000Fu, ha & 0x00F000F0u, hb & 0x00F000F0u, qf[2 * G + 1][0],
-                        qf[2 * G + 1][1]);
-          const float fa = fa4[G], fb = fb4[G];
-          s[0] = G ? fmaf(fa, d[0], s[0]) : fa * d[0];
-          s[1] = G ? fmaf(fa, d[1], s[1]) : fa * d[1];
-          s[2] = G ? fmaf(fb, d[2], s[2]) : fb * d[2];
-          s[3] = G ? fmaf(fb, d[3], s[3]) : fb * d[3];
+        for (int h = 0; h < kStep; ++h) {
+          const uint32_t tb = base + h * R::kTileBytes;
+          const uint4 wa = lds128(tb + lane * 16), wb = lds128(tb + 512 + lane * 16);
+          const uint32_t ka[4] = {wa.x, wa.y, wa.z, wa.w}, kb[4] = {wb.x, wb.y, wb.z, wb.w};
+          const uint4 sa = lds128(scales + h * R::kScaleBytes + t0 * 16), sb = lds128(scales + h * R::kScaleBytes + t1 * 16);
+          const float fa[4] = {__uint_as_float(sa.x), __uint_as_float(sa.y), __uint_as_float(sa.z), __uint_as_float(sa.w)};
+          const float fb[4] = {__uint_as_float(sb.x), __uint_as_float(sb.y), __uint_as_float(sb.z), __uint_as_float(sb.w)};
+          const uint32_t ra = lds32(tb + 2048 + t0 * 8 + (c & 1) * 4), rb = lds32(tb + 2048 + t1 * 8 + (c & 1) * 4);
+          s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.f;
+          mma_bf16_16816(s[h], ra, rb, ra, rb, off_b[0], off_b[1]);
+#pragma unroll
+          for (int G = 0; G < 4; ++G) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t ha = ka[G] >> 8, hb = kb[G] >> 8;
+            mma_f16_16816(d, ka[G] & 0x000F000Fu, kb[G] & 0x000F000Fu, ka[G] & 0x00F000F0u, kb[G] & 0x00F000F0u,
+                          qf[2 * G][0], qf[2 * G][1]);
+            mma_f16_16816(d, ha & 0x000F000Fu, hb & 0x000F000Fu, ha & 0x00F000F0u, hb & 0x00F000F0u, qf[2 * G + 1][0],
+                          qf[2 * G + 1][1]);
+            s[h][0] = fmaf(fa[G], d[0], s[h][0]);
+            s[h][1] = fmaf(fa[G], d[1], s[h][1]);
+            s[h][2] = fmaf(fb[G], d[2], s[h][2]);
+            s[h][3] = fmaf(fb[G], d[3], s[h][3]);
+          }
         }
       } else {
         t0 = tq;
@@ -494,63 +563,77 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_
             mma_bf16_16816(sa, a0, a1, a2, a3, qf[kk][0], qf[kk][1]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = sa[i] + sb[i];
+        for (int i = 0; i < 4; ++i) s[0][i] = sa[i] + sb[i];
       }
-      if (nvalid < kTileTokens) {
-        if (t0 >= nvalid) s[0] = s[1] = kNegInf;
-        if (t1 >= nvalid) s[2] = s[3] = kNegInf;
-      }
-      if constexpr (kAcc) {  // the logits of the tile, for the weights once lse is known
-        const int64_t slot = pair * p.k * bs + (int64_t)(j0 * tpb + warp + kWarps * nt) * kTileTokens;
-        float* z0 = p.z + (slot + t0) * g + ta;
-        float* z1 = p.z + (slot + t1) * g + ta;
-        if (ta < g) {
-          z0[0] = s[0] * sl2[0];
-          z1[0] = s[2] * sl2[0];
+      if (part) {
+#pragma unroll
+        for (int h = 0; h < kStep; ++h) {
+          if (t0 >= nv[h]) s[h][0] = s[h][1] = kNegInf;
+          if (t1 >= nv[h]) s[h][2] = s[h][3] = kNegInf;
         }
-        if (ta + 1 < g) {
-          z0[1] = s[1] * sl2[1];
-          z1[1] = s[3] * sl2[1];
+      }
+      if constexpr (kAcc) {  // the logits of the tiles, for the weights once lse is known
+#pragma unroll
+        for (int h = 0; h < kStep; ++h) {
+          if (nv[h] > 0) {
+            const int tile = (warp + kWarps * st) * kStep + h;
+            const int64_t slot0 = (int64_t)pair * p.k * bs + (int64_t)(j0 * tpb + tile) * kTileTokens;
+            float* z0 = p.z + (slot0 + t0) * g + ta;
+            float* z1 = p.z + (slot0 + t1) * g + ta;
+            if (ta < g) {
+              z0[0] = s[h][0] * sl2[0];
+              z1[0] = s[h][2] * sl2[0];
+            }
+            if (ta + 1 < g) {
+              z0[1] = s[h][1] * sl2[1];
+              z1[1] = s[h][3] * sl2[1];
+            }
+          }
         }
       }
       weigh(a, s, sl2, pr);
       if constexpr (kInt4) {
-        const uint32_t p0 = movmatrix_trans(pack_f16x2(pr[0], pr[1])), p1 = movmatrix_trans(pack_f16x2(pr[2], pr[3]));
-        const uint4 va = lds128(scales + 256 + c * 16), vb = lds128(scales + 256 + 64 + c * 16);
-        const uint32_t pb[4][2] = {{hmul2(p0, va.x), hmul2(p1, vb.x)}, {hmul2(p0, va.y), hmul2(p1, vb.y)},
-                                   {hmul2(p0, va.z), hmul2(p1, vb.z)}, {hmul2(p0, va.w), hmul2(p1, vb.w)}};
-        // value codes: tokens c, c + 4, c + 8, c + 12; the lane's 4 channels of
-        // each group.  Two tokens' halfwords side by side, then nibbles as
-        // n 2^-24 and n 2^-20 like the keys'; 8 times the weights' sum, taken
-        // by a product with a row of ones for each group, comes off at the
-        // end (a warp's tiles are few enough for it to cost nothing).
-        uint2 x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = c + 4 * i;
-          x[i] = lds64(base + 1024 + t * 64 + (((tq >> 1) ^ (t & 2)) << 4) + (tq & 1) * 8);
-        }
+        for (int h = 0; h < kStep; ++h) {
+          const uint32_t tb = base + h * R::kTileBytes, sc = scales + h * R::kScaleBytes + 256;
+          const uint32_t p0 = movmatrix_trans(pack_f16x2(pr[h][0], pr[h][1]));
+          const uint32_t p1 = movmatrix_trans(pack_f16x2(pr[h][2], pr[h][3]));
+          const uint4 va = lds128(sc + c * 16), vb = lds128(sc + 64 + c * 16);
+          const uint32_t pb[4][2] = {{hmul2(p0, va.x), hmul2(p1, vb.x)}, {hmul2(p0, va.y), hmul2(p1, vb.y)},
+                                     {hmul2(p0, va.z), hmul2(p1, vb.z)}, {hmul2(p0, va.w), hmul2(p1, vb.w)}};
+          // value codes: tokens c, c + 4, c + 8, c + 12; the lane's 4 channels
+          // of each group.  Two tokens' halfwords side by side, then nibbles as
+          // n 2^-24 and n 2^-20 like the keys'; 8 times the weights' sum, taken
+          // by a product with a row of ones for each group, comes off at the
+          // end (a warp's tiles are few enough for it to cost nothing).
+          uint2 x[4];
 #pragma unroll
-        for (int G = 0; G < 4; ++G) {
-          const uint32_t sel = (G & 1) ? 0x7632u : 0x5410u;
-          const uint32_t u01 = __byte_perm(G < 2 ? x[0].x : x[0].y, G < 2 ? x[1].x : x[1].y, sel);
-          const uint32_t u23 = __byte_perm(G < 2 ? x[2].x : x[2].y, G < 2 ? x[3].x : x[3].y, sel);
-          const uint32_t h01 = u01 >> 8, h23 = u23 >> 8;
-          const uint32_t one = tq == G ? 0x3C003C00u : 0u;
-          mma_f16_16816(a.o[2 * G], u01 & 0x000F000Fu, u01 & 0x00F000F0u, u23 & 0x000F000Fu, u23 & 0x00F000F0u, pb[G][0],
-                        pb[G][1]);
-          mma_f16_16816(a.o[2 * G + 1], h01 & 0x000F000Fu, h01 & 0x00F000F0u, h23 & 0x000F000Fu, h23 & 0x00F000F0u,
-                        pb[G][0], pb[G][1]);
-          mma_f16_16816(a.sums, one, 0u, one, 0u, pb[G][0], pb[G][1]);
+          for (int i = 0; i < 4; ++i) {
+            const int t = c + 4 * i;
+            x[i] = lds64(tb + 1024 + t * 64 + (((tq >> 1) ^ (t & 2)) << 4) + (tq & 1) * 8);
+          }
+#pragma unroll
+          for (int G = 0; G < 4; ++G) {
+            const uint32_t sel = (G & 1) ? 0x7632u : 0x5410u;
+            const uint32_t u01 = __byte_perm(G < 2 ? x[0].x : x[0].y, G < 2 ? x[1].x : x[1].y, sel);
+            const uint32_t u23 = __byte_perm(G < 2 ? x[2].x : x[2].y, G < 2 ? x[3].x : x[3].y, sel);
+            const uint32_t h01 = u01 >> 8, h23 = u23 >> 8;
+            const uint32_t one = tq == G ? 0x3C003C00u : 0u;
+            mma_f16_16816(a.o[2 * G], u01 & 0x000F000Fu, u01 & 0x00F000F0u, u23 & 0x000F000Fu, u23 & 0x00F000F0u,
+                          pb[G][0], pb[G][1]);
+            mma_f16_16816(a.o[2 * G + 1], h01 & 0x000F000Fu, h01 & 0x00F000F0u, h23 & 0x000F000Fu, h23 & 0x00F000F0u,
+                          pb[G][0], pb[G][1]);
+            mma_f16_16816(a.sums, one, 0u, one, 0u, pb[G][0], pb[G][1]);
+          }
         }
       } else {
         // weights as the sum of two bf16 numbers (16 bits): a single bf16
         // weight would cost as much accuracy as the final rounding
-        const uint32_t h0 = pack_bf16x2(pr[0], pr[1]), h1 = pack_bf16x2(pr[2], pr[3]);
+        const uint32_t h0 = pack_bf16x2(pr[0][0], pr[0][1]), h1 = pack_bf16x2(pr[0][2], pr[0][3]);
         const uint32_t pb0 = movmatrix_trans(h0), pb1 = movmatrix_trans(h1);
-        const uint32_t pl0 = movmatrix_trans(pack_bf16x2(pr[0] - lo_f(h0), pr[1] - hi_f(h0)));
-        const uint32_t pl1 = movmatrix_trans(pack_bf16x2(pr[2] - lo_f(h1), pr[3] - hi_f(h1)));
-        const uint32_t mlo = tok_mask(ta, nvalid), mhi = tok_mask(ta + 8, nvalid);
+        const uint32_t pl0 = movmatrix_trans(pack_bf16x2(pr[0][0] - lo_f(h0), pr[0][1] - hi_f(h0)));
+        const uint32_t pl1 = movmatrix_trans(pack_bf16x2(pr[0][2] - lo_f(h1), pr[0][3] - hi_f(h1)));
+        const uint32_t mlo = tok_mask(ta, nv[0]), mhi = tok_mask(ta + 8, nv[0]);
         const int vt = (lane & 7) + ((lane >> 4) << 3), vsel = (lane >> 3) & 1;
 #pragma unroll
         for (int dm = 0; dm < 8; ++dm) {
@@ -559,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_
           const int ch = (d0 & 63) >> 3;
           uint32_t a0, a1, a2, a3;
           ldmatrix_x4_trans(box + vt * 128 + ((ch ^ (vt & 7)) << 4), a0, a1, a2, a3);
-          if (nvalid < kTileTokens) {
+          if (part) {
             a0 &= mlo;
             a1 &= mlo;
             a2 &= mhi;
@@ -571,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_
       }
     }
     __syncwarp();
-    issue(nt + kStages, slot);
+    issue(st + kStages, slot);
     slot = slot == (kStages - 1) * R::kStageBytes ? 0u : slot + R::kStageBytes;
   }
   cp_async_wait<0>();
@@ -655,12 +738,15 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_
     }
   };
   if (nchunks == 1) {
+#pragma unroll 1
     for (int j = 0; j < g; ++j) finish(j, combined(j), s_cden[j], s_cm[j]);
-    return;
+    __syncthreads();  // the next pair's ring takes the combine area
+    continue;
   }
 
   // this chunk's partial; the pair's last chunk merges all of them
-  float* part = p.partials + (pair * p.max_chunks + chunk) * (int64_t)g * kPartStride;
+  float* part = p.partials + ((int64_t)pair * p.max_chunks + chunk) * g * kPartStride;
+#pragma unroll 1
   for (int j = 0; j < g; ++j) {
     part[j * kPartStride + d] = combined(j);
     if (d == 0) {
@@ -673,14 +759,14 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_
   __syncthreads();
   if (tid == 0) s_last = (count_chunk(&p.counters[pair]) == (unsigned)(nchunks - 1));
   __syncthreads();
-  if (!s_last) return;
+  if (!s_last) continue;
   if (tid == 0) p.counters[pair] = 0u;  // ready for the next call
   // The partials are staged in shared memory, a batch of chunks at a time;
   // thread j < g folds head j's maxima and sums and leaves one weight per
   // (chunk, head); every thread folds its output channel.
   const int rec = g * kPartStride;
   const int per_batch = R::kPipe / (4 * rec);
-  const float4* src4 = reinterpret_cast<const float4*>(p.partials + pair * p.max_chunks * (int64_t)rec);
+  const float4* src4 = reinterpret_cast<const float4*>(p.partials + (int64_t)pair * p.max_chunks * rec);
   const float* stage = reinterpret_cast<const float*>(smem);
   const uint32_t stage_s = smem_u32(smem);
   float num[kMaxGroup];
@@ -701,11 +787,13 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_
     if (tid < g) {
       const int j = tid;
       float Mb = kNegInf;
+#pragma unroll 4
       for (int cc = 0; cc < nbat; ++cc) Mb = fmaxf(Mb, stage[(cc * g + j) * kPartStride + kHeadDim]);
       const float Mr = s_mr[j];
       const float Mn = fmaxf(Mr, Mb);
       const float al = s_den[j] == 0.f ? 0.f : exp2f(Mr - Mn);
       float dd = s_den[j] * al;
+#pragma unroll 4
       for (int cc = 0; cc < nbat; ++cc) {
         const float* r = stage + (cc * g + j) * kPartStride;
         const float e = r[kHeadDim + 1] == 0.f ? 0.f : exp2f(r[kHeadDim] - Mn);
@@ -720,6 +808,7 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_
 #pragma unroll
     for (int j = 0; j < kMaxGroup; ++j)
       if (j < g) num[j] *= s_a[j];
+#pragma unroll 2
     for (int cc = 0; cc < nbat; ++cc) {
       const float* rc = stage + cc * g * kPartStride + d;
 #pragma unroll
@@ -731,6 +820,7 @@ __global__ void __launch_bounds__(kThreads, kInt4 ? KIN_KV4_CTAS_PER_SM : 3) kv_
 #pragma unroll
   for (int j = 0; j < kMaxGroup; ++j)
     if (j < g) finish(j, num[j], s_den[j], s_mr[j]);
+  }
 }
 
 // The weights of the attended tokens, once every lse is known: one thread per
@@ -769,7 +859,7 @@ static cudaError_t launch_kv_attn_as(const KvAttnParams& p, cudaStream_t s) {
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), 16 + 2 * kInt4 + kAcc, Ring<kInt4>::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t pairs = (int64_t)p.B * p.Hkv;
-  e = launch_pdl(kernel, dim3((unsigned)(pairs * p.max_chunks)), dim3(kThreads), Ring<kInt4>::kSmem, s, p);
+  e = launch_pdl(kernel, dim3((unsigned)((p.slots + p.per - 1) / p.per)), dim3(kThreads), Ring<kInt4>::kSmem, s, p);
   if (e != cudaSuccess || !kAcc) return e;
   const int64_t per = (int64_t)p.k * p.bs;
   return launch_pdl(kv_weights_kernel, dim3((unsigned)(pairs * ((per + 255) / 256))), dim3(256), 0, s, p);
