@@ -652,23 +652,52 @@ kin_status means_layout(const kin_dims& d, const KvView& kv, const void* means, 
 // The two share a buffer, a page pool included.
 bool same_cache(const KvView& a, const KvView& b) { return a.k == b.k || a.v == b.v || a.k == b.v || a.v == b.k; }
 
-// How the attention cuts the (pair, kept block) slots into ranges, one per
-// CTA.  Selected blocks: as many even ranges as fill whole waves of
-// kKvCtasPerSm CTAs per SM, so that all CTAs end together.  Every block: the
-// lengths are only known on the device and a range may be empty, so ranges
-// hold at most 1024 tokens.  Never less than 128 tokens (a step of each
-// warp), nor more than a pair or kKvItemTiles tiles.
-int kv_range_blocks(const kin_dims& d, int k, bool dense) {
+// How the attention cuts the (pair, kept block) slots into ranges of `per`
+// blocks, one per CTA.  A pair's slots are padded to `stride`: a multiple of
+// per (aligned: no range crosses a pair), or k itself (ranges that run on into
+// the next pair, so that every resident CTA gets the same).
+struct KvSplit {
+  int per, stride;
+};
+
+// Chosen by an estimate in microseconds, from timings of 4-bit caches (bf16
+// tiles take three times as long, which leaves the order as it is): a CTA
+// spends 4.5 on a range, 2.5 more where ranges of a pair are merged, and 0.12
+// a tile alone, 0.064 times the SM's CTAs when they share it.  Against even
+// ranges over the pairs' borders, 256 pairs of 32, 128 and 256 tiles took 8.7,
+// 20.6 and 38.0 with one range each and 17.7, 28.4 and 41.9 without.
+KvSplit kv_split(const kin_dims& d, int k, bool dense) {
   const int tpb = d.block_size / kTileTokens;
-  const int64_t slots = (int64_t)pairs_of(d) * k;
-  int64_t cap = (dense ? 64 : kKvItemTiles) / tpb;
-  if (cap > k) cap = k;
+  const int64_t pairs = pairs_of(d);
+  const int most = (dense ? kKvItemTiles / 2 : kKvItemTiles) / tpb;  // dense: lengths unknown here, ranges may be empty
+  const int least = (8 + tpb - 1) / tpb;                             // a step of each warp
   const int64_t wave = (int64_t)kTargetSMs * kKvCtasPerSm;
-  const int64_t waves = (slots + wave * cap - 1) / (wave * cap);
-  int64_t per = (slots + wave * waves - 1) / (wave * waves);
-  const int least = (8 + tpb - 1) / tpb;
-  if (per < least) per = least;
-  return (int)(per < cap ? per : cap);
+  auto range_us = [&](int64_t tiles, int64_t per_sm, bool merged) {
+    const double shared = 0.064 * (double)per_sm;
+    return (double)tiles * (shared > 0.12 ? shared : 0.12) + (merged ? 7.0 : 4.5);
+  };
+  KvSplit best{0, 0};
+  double best_us = 0;
+  const int c0 = (k + most - 1) / most;
+  for (int c = c0; c < c0 + 64; ++c) {
+    const int per = (k + c - 1) / c;
+    if (c > c0 && per < least) break;
+    const int64_t n = pairs * ((k + per - 1) / per), full = n / wave, rest = n % wave;
+    double us = (double)full * range_us((int64_t)per * tpb, kKvCtasPerSm, per < k);
+    if (rest) us += range_us((int64_t)per * tpb, (rest + kTargetSMs - 1) / kTargetSMs, per < k);
+    if (!best.per || us < best_us) {
+      best = KvSplit{per, (k + per - 1) / per * per};
+      best_us = us;
+    }
+  }
+  const int64_t slots = pairs * k;
+  const int64_t waves = (slots + wave * most - 1) / (wave * most);
+  const int64_t per = (slots + wave * waves - 1) / (wave * waves);
+  if (!dense && per >= least && per < k) {
+    const double us = (double)waves * (range_us(per * tpb, kKvCtasPerSm, true) + 7.0);
+    if (us < best_us) best = KvSplit{(int)per, k};
+  }
+  return best;
 }
 
 // The slots of the kept blocks of a pair: at most k_blocks, at most all.
@@ -678,7 +707,9 @@ int kv_slots(const kin_dims& d, int k_blocks) {
 }
 
 // CTAs whose ranges a pair's slots may meet.
-int kv_max_chunks(int k, int per) { return (k + per - 2) / per + 1; }
+int kv_max_chunks(int k, const KvSplit& s) {
+  return s.stride % s.per == 0 ? s.stride / s.per : (k + s.per - 2) / s.per + 1;
+}
 
 struct KvWs {
   size_t counters, partials, z, lse2, total;
@@ -694,7 +725,7 @@ KvWs kv_ws_layout(const kin_dims& d, int k_blocks, bool acc) {
   w.counters = 0;
   off = k_blocks >= 2 ? ws_layout(d, k_blocks).total : align_up(pairs * sizeof(uint32_t));
   w.partials = off;
-  off = align_up(off + pairs * (size_t)kv_max_chunks(k, kv_range_blocks(d, k, k_blocks == 0)) * g * kPartStride * sizeof(float));
+  off = align_up(off + pairs * (size_t)kv_max_chunks(k, kv_split(d, k, k_blocks == 0)) * g * kPartStride * sizeof(float));
   w.z = off;
   if (acc) off = align_up(off + pairs * (size_t)k * d.block_size * g * sizeof(float));
   w.lse2 = off;
@@ -833,11 +864,15 @@ KIN_EXPORT kin_status kin_kv_decode_attn(const kin_dims* dims, const void* q, co
   p.bs = dims->block_size;
   p.k_row = k_blocks;
   p.k = kv_slots(*dims, k_blocks);
-  p.slots = pairs_of(*dims) * p.k;
-  p.per = kv_range_blocks(*dims, p.k, k_blocks == 0);
-  p.max_chunks = kv_max_chunks(p.k, p.per);
+  const KvSplit split = kv_split(*dims, p.k, k_blocks == 0);
+  p.per = split.per;
+  p.stride = split.stride;
+  if ((int64_t)pairs_of(*dims) * p.stride >= (int64_t)1 << 31) return KIN_ERR_CAPACITY;
+  p.slots = pairs_of(*dims) * p.stride;
+  p.max_chunks = kv_max_chunks(p.k, split);
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)kHeadDim);
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.two24 = 1u << 24;
   return from_cuda(launch_kv_attn(p, static_cast<cudaStream_t>(stream)));
 }
 

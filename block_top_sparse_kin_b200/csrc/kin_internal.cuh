@@ -400,10 +400,12 @@ struct KvAttnParams {
   int32_t* dev_status;
   int B, Hkv, Hq, g, bs;
   int k, k_row;            // kept blocks a pair may have; stride of sel_idx
-  int slots;               // pairs x k
+  int stride;              // a pair's slots: k, or padded to a multiple of per
+  int slots;               // pairs x stride
   int per;                 // slots of a CTA
   int max_chunks;          // CTAs that a pair's slots may meet
   float scale_log2;
+  uint32_t two24;          // 2^24, where the kernel cannot see its value
 };
 
 // Eviction: the kept tokens of every pair, then their move.

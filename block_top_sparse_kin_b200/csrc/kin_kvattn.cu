@@ -25,18 +25,25 @@ namespace {
 
 #define kNegInf (-__int_as_float(0x7f800000))
 
+#ifndef KIN_KV4_STEP
+#define KIN_KV4_STEP 2
+#endif
 #ifndef KIN_KV4_STAGES
 #define KIN_KV4_STAGES 3
 #endif
-constexpr int kWarps = 4;
+#ifndef KIN_KV_WARPS
+#define KIN_KV_WARPS 4
+#endif
+constexpr int kWarps = KIN_KV_WARPS;
 constexpr int kThreads = kWarps * 32;
+constexpr int kDims = kHeadDim / kThreads;  // output channels of a thread
 constexpr int kRowPad = kHeadDim + 4;
 constexpr int kHalfBox = 16 * 64 * 2;
 
 template <bool kInt4>
 struct Ring {
   // tiles of 16 tokens that a warp takes at a step
-  static constexpr int kStep = kInt4 ? 2 : 1;
+  static constexpr int kStep = kInt4 ? KIN_KV4_STEP : 1;
   // bf16: K0 K1 V0 V1 half tiles of 16 rows x 64 channels.  4 bit: 16 rows of
   // 64 bytes of key codes, of value codes, then 16 x 4 scales of each.
   static constexpr int kTileBytes = kInt4 ? 2 * 16 * kCodeBytes + 2 * 16 * kGroups * 2 : 4 * kHalfBox;
@@ -45,7 +52,8 @@ struct Ring {
   // 4 bit, per warp and tile behind the ring: the tile's key scales as fp32
   // [16][4] and its value scales as fp16 pairs [8 token pairs][4]
   static constexpr int kScaleBytes = kInt4 ? 256 + 128 : 0;
-  static constexpr int kPipe = kWarps * (kStages * kStageBytes + kStep * kScaleBytes);
+  static constexpr int kWarpBytes = kStages * kStageBytes + kStep * kScaleBytes;
+  static constexpr int kPipe = kWarps * kWarpBytes;
   static constexpr int kComb = kWarps * kMaxGroup * kRowPad * 4;
   static constexpr int kSmem = (kPipe > kComb ? kPipe : kComb) + 1024;
 };
@@ -74,6 +82,8 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+
+__device__ __forceinline__ uint32_t part_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 __device__ __forceinline__ unsigned count_chunk(uint32_t* counter) {
   unsigned v;
@@ -195,6 +205,14 @@ __device__ __forceinline__ void weigh(Acc& a, const float (&s)[N][4], const floa
 
 }  // namespace
 
+constexpr uint32_t kPartial = 0x80000000u;
+
+// Tile i of a warp, in its CTA's range: steps are dealt to the warps in turn.
+template <int kStep>
+__device__ __forceinline__ int warp_tile(int warp, int i) {
+  return (warp + kWarps * (i / kStep)) * kStep + i % kStep;
+}
+
 template <bool kInt4, bool kAcc>
 __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnParams p) {
   using R = Ring<kInt4>;
@@ -203,52 +221,70 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   __shared__ float s_m[kWarps][kMaxGroup], s_l[kWarps][kMaxGroup];
   __shared__ int s_last;
   constexpr int kMaxMergeWeights = R::kPipe / (4 * kPartStride);
-  __shared__ float s_mr[kMaxGroup], s_den[kMaxGroup], s_a[kMaxGroup], s_w[kMaxMergeWeights];
+  __shared__ float s_mr[kMaxGroup], s_den[kMaxGroup], s_inv[kMaxGroup], s_a[kMaxGroup], s_w[kMaxMergeWeights];
   __shared__ float s_ww[kWarps][kMaxGroup], s_cm[kMaxGroup], s_cden[kMaxGroup];
+  // per warp: its tiles' rows (kPartial: less than 16 of them valid) and valid rows
+  __shared__ __align__(8) uint32_t s_rows[kWarps][64];
+  __shared__ uint8_t s_valid[kWarps][64];
+  // 4 bit: the group's queries in fp16, per group of channels -8 times their sum, the logits' scales
+  __shared__ __align__(16) uint32_t s_q[kInt4 ? kMaxGroup * 64 : 4];
+  __shared__ float s_off[kMaxGroup][4], s_sl2[kMaxGroup];
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = p.g, bs = p.bs, Lcap = p.kv.Lcap;
   pdl_wait();  // the selection comes from the select kernels
   pdl_trigger_early();
-  const int tpb = bs / kTileTokens;
-  const int n = lane >> 2, c = lane & 3;
-  const int tq = lane >> 2, ta = 2 * c;
+  const int lbs = 31 - __clz(bs), ltpb = lbs - 4;  // log2 of a block's tokens and of its tiles
+  const int c = lane & 3, tq = lane >> 2, ta = 2 * c;
+
+  const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * R::kWarpBytes);
+  const uint32_t scales = ring + kStages * R::kStageBytes;
+  const uint32_t rows_s = smem_u32(s_rows[warp]);
+  // 4 bit: a row's 4 pieces of 16 bytes of codes lie in token order, pieces 2
+  // and 3 swapped with 0 and 1 in every second pair of rows: both the keys'
+  // 16-byte reads (two rows of different parity in 8 lanes) and the values'
+  // 8-byte reads (four rows, both parities, both orders, in 16 lanes) are then
+  // free of bank conflicts, with the tokens' order below
+  const uint32_t code_dst = ring + tq * 64 + ((c ^ (tq & 2)) << 4);
+  const uint32_t scale_dst = ring + 2048 + lane * 8;
+  // k slots 2c, 2c + 1, 2c + 8, 2c + 9 of the second product are tokens c, 4 +
+  // (c ^ 1), 8 + c and 12 + (c ^ 1) of the tile: so is the order of its rows
+  const int t0 = kInt4 ? ((tq & 1) ? 4 + ((tq >> 1) ^ 1) : tq >> 1) : tq, t1 = t0 + 8;
 
   // This CTA's range of the (pair, kept block) slots, cut at pair boundaries:
   // blocks [j0, j1) of one pair at a time.
   const int hi_slot = min((int)(blockIdx.x + 1) * p.per, p.slots);
   for (int at = blockIdx.x * p.per; at < hi_slot;) {
-  const int pair = at / p.k, j0 = at - pair * p.k;
-  const int j1 = min(p.k, hi_slot - pair * p.k);
-  at = (pair + 1) * p.k;
+  const int pair = at / p.stride, j0 = at - pair * p.stride;
+  const int j1 = min(p.k, hi_slot - pair * p.stride);
+  at = (pair + 1) * p.stride;
+  const int b = pair / p.Hkv, h = pair - b * p.Hkv;
+  const int64_t qh0 = (int64_t)b * p.Hq + (int64_t)h * g;
   // lane l's tiles l and l + 32 of this warp (steps warp, warp + W, .. of the
   // range, kStep tiles each): their block indices are requested before the
   // length and count, whose round trip they would follow
-  int my_tile[2], blk[2];
+  int blk[2];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    const int i = lane + 32 * r;
-    my_tile[r] = (warp + kWarps * (i / kStep)) * kStep + i % kStep;
-    const int j = j0 + my_tile[r] / tpb;
+    const int j = j0 + (warp_tile<kStep>(warp, lane + 32 * r) >> ltpb);
     blk[r] = j;
     if (p.sel_idx) blk[r] = j < j1 ? __ldg(p.sel_idx + (int64_t)pair * p.k_row + j) : -1;
   }
-  const int b = pair / p.Hkv, h = pair - b * p.Hkv;
-  const int64_t qh0 = (int64_t)b * p.Hq + (int64_t)h * g;
-  const __nv_bfloat16* qrow = p.q + (qh0 + (n < g ? n : 0)) * kHeadDim;
-  uint4 qw[4];  // 4 bit
-#pragma unroll
-  for (int G = 0; G < 4 && kInt4; ++G) qw[G] = __ldg(reinterpret_cast<const uint4*>(qrow + 32 * G + 8 * c));
+  // 4 bit: thread t's 8 query channels, 8 (t % 16) .. of head t / 16
+  uint4 qw = make_uint4(0u, 0u, 0u, 0u);
+  if constexpr (kInt4) {
+    if ((tid >> 4) < g) qw = __ldg(reinterpret_cast<const uint4*>(p.q + (qh0 + (tid >> 4)) * kHeadDim) + (tid & 15));
+  }
   const int L = __ldg(p.seq_lens + b);
   const bool bad_len = L < 1 || L > Lcap;
-  const int nb = bad_len ? 0 : (L + bs - 1) / bs;
+  const int nb = bad_len ? 0 : (L + bs - 1) >> lbs;
   int cnt = p.sel_idx ? __ldg(p.sel_cnt + pair) : nb;
   if (bad_len) cnt = 0;
   if (cnt > p.k) cnt = p.k;
   if (cnt <= 0) {  // nothing to attend to: out = 0, lse = -inf
     if (j0 == 0) {
-      for (int j = 0; j < g; ++j) p.out[(qh0 + j) * kHeadDim + tid] = __float2bfloat16_rn(0.f);
+      for (int d = tid; d < g * kHeadDim; d += kThreads) p.out[qh0 * kHeadDim + d] = __float2bfloat16_rn(0.f);
       if (tid < g) {
         if (p.lse) p.lse[qh0 + tid] = kNegInf;
         if (kAcc) p.lse2[qh0 + tid] = kNegInf;
@@ -257,60 +293,53 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
     }
     continue;
   }
-  const int ntiles = (min(j1, cnt) - j0) * tpb;
+  const int ntiles = (min(j1, cnt) - j0) << ltpb;
   if (ntiles <= 0) continue;
   // the pair's ranges that hold a kept block, and this one's place among them
-  const int first_cta = pair * p.k / p.per;
-  const int nchunks = (pair * p.k + cnt - 1) / p.per - first_cta + 1, chunk = blockIdx.x - first_cta;
+  const int first_cta = pair * p.stride / p.per;
+  const int nchunks = (pair * p.stride + cnt - 1) / p.per - first_cta + 1, chunk = blockIdx.x - first_cta;
 
-  // lane n holds its tiles' first rows (a cache of 2^31 rows is larger than
-  // the memory) and valid rows; bit n of `partial` marks a tile of less than 16
+  // the warp's tiles' first rows (a cache of 2^31 rows is larger than the
+  // memory); a tile of less than 16 rows is marked and their number kept aside
   const int n_w = warp * kStep < ntiles ? (ntiles - 1 - warp * kStep) / (kWarps * kStep) + 1 : 0;  // steps
-  uint32_t my_row[2] = {0u, 0u}, partial[2];
-  int my_nvalid[2] = {0, 0};
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    if (my_tile[r] < ntiles) {
-      const int tok = blk[r] * bs + (my_tile[r] % tpb) * kTileTokens;
+    const int tile = warp_tile<kStep>(warp, lane + 32 * r);
+    uint32_t row = 0u;
+    int nv = 0;
+    if (tile < ntiles) {
+      const int tok = (blk[r] << lbs) + ((tile & ((1 << ltpb) - 1)) << 4);
       const bool there = blk[r] >= 0 && blk[r] < nb;
-      int64_t row = -1;
-      if (there && tok < L) row = kv_row(p.kv.pages, b, h, p.Hkv, Lcap, bs, tok);
-      if (!there || (tok < L && row < 0)) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
-      my_nvalid[r] = row < 0 ? 0 : min(kTileTokens, L - tok);
-      my_row[r] = row < 0 ? 0u : (uint32_t)row;
+      bool good = there && tok < L;
+      if (good) {
+        if (p.kv.pages.table) {
+          const int page = __ldg(p.kv.pages.table + (int64_t)b * p.kv.pages.max_blocks + blk[r]);
+          good = page >= 0 && page < p.kv.pages.num_pages;
+          row = ((uint32_t)(page * p.Hkv + h) << lbs) + (tok & (bs - 1));
+        } else {
+          row = (uint32_t)pair * (uint32_t)Lcap + (uint32_t)tok;
+        }
+      }
+      if (!there || (tok < L && !good)) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
+      if (good) nv = min(kTileTokens, L - tok);
+      if (!good) row = 0u;
     }
-    partial[r] = __ballot_sync(0xffffffffu, my_nvalid[r] < kTileTokens);
+    s_rows[warp][lane + 32 * r] = row | (nv < kTileTokens ? kPartial : 0u);
+    s_valid[warp][lane + 32 * r] = (uint8_t)nv;
   }
-  auto tile_row = [&](int i) { return __shfl_sync(0xffffffffu, i < 32 ? my_row[0] : my_row[1], i & 31); };
-  auto tile_valid = [&](int i) { return __shfl_sync(0xffffffffu, i < 32 ? my_nvalid[0] : my_nvalid[1], i & 31); };
-  auto tile_partial = [&](int i) { return (i < 32 ? partial[0] : partial[1]) >> (i & 31); };
+  __syncwarp();
 
-  const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * (kStages * R::kStageBytes + kStep * R::kScaleBytes));
-  const uint32_t scales = ring + kStages * R::kStageBytes;
-  // 4 bit: 64 pieces of 16 bytes of key codes and of value codes, 8 bytes of
-  // scales for each row.  Key row i of the tile holds token (i & 8) + 4 (i & 1)
-  // + (i & 7) / 2, so that the tile's k slots 2c, 2c + 1 of the second product
-  // are tokens c, c + 4 (and 8 + c, 12 + c); the value rows stay in token
-  // order, their pieces 2 and 3 swapped with 0 and 1 in every second pair of
-  // rows, which keeps their 8-byte reads free of bank conflicts.
-  const int it = lane >> 2, icol = lane & 3;
-  const uint32_t k_dst = ring + (((it & 3) << 1) | (it >> 2)) * 64 + icol * 16;
-  const uint32_t v_dst = ring + 1024 + it * 64 + ((icol ^ (it & 2)) << 4);
-  const uint32_t s_dst = ring + 2048 + lane * 8;
-  const uint8_t* k_src = p.kv.k + lane * 16;
-  const uint8_t* v_src = p.kv.v + lane * 16;
-  const uint16_t* s_src = (lane < 16 ? p.kv.ks : p.kv.vs) + (lane & 15) * kGroups;
-  auto issue_tile = [&](int nt, uint32_t slot) {  // slot: byte offset of the tile's place in the ring
-    const uint32_t row = tile_row(nt);
-    if (!(tile_partial(nt) & 1u)) {
+  auto issue_tile = [&](int nt, uint32_t row, uint32_t slot) {  // slot: byte offset of the tile's place in the ring
+    if (row < kPartial) {
       if constexpr (kInt4) {
-        const uint8_t* ks = k_src + (uint64_t)row * kCodeBytes;
-        const uint8_t* vs = v_src + (uint64_t)row * kCodeBytes;
-        cp_async16(k_dst + slot, ks, 16u);
-        cp_async16(k_dst + slot + 512, ks + 512, 16u);
-        cp_async16(v_dst + slot, vs, 16u);
-        cp_async16(v_dst + slot + 512, vs + 512, 16u);
-        cp_async8(s_dst + slot, s_src + (uint64_t)row * kGroups, 8u);
+        const uint8_t* ks = p.kv.k + (uint64_t)row * kCodeBytes + lane * 16;
+        const uint8_t* vs = p.kv.v + (uint64_t)row * kCodeBytes + lane * 16;
+        const uint16_t* ss = (lane < 16 ? p.kv.ks : p.kv.vs) + ((uint64_t)row + (lane & 15)) * kGroups;
+        cp_async16(code_dst + slot, ks, 16u);
+        cp_async16(code_dst + slot + 512, ks + 512, 16u);
+        cp_async16(code_dst + slot + 1024, vs, 16u);
+        cp_async16(code_dst + slot + 1536, vs + 512, 16u);
+        cp_async8(scale_dst + slot, ss, 8u);
       } else {
         const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.kv.k) + (uint64_t)row * kHeadDim;
         const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.kv.v) + (uint64_t)row * kHeadDim;
@@ -324,21 +353,23 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
         }
       }
     } else {  // rows behind the length: zeros, nothing read (the address stays on a valid row)
-      const int nv = tile_valid(nt);
+      const int nv = s_valid[warp][nt];
+      row &= ~kPartial;
       if constexpr (kInt4) {
         // a tile without any row: its scales become zeros, its codes may be
         // anything (every nibble is a finite number and its weight is zero)
         if (nv > 0) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int t = it + 8 * i;
-            const int64_t from = (int64_t)row * kCodeBytes + (t < nv ? 512 * i : -it * 64);
-            cp_async16(k_dst + slot + 512 * i, k_src + from, t < nv ? 16u : 0u);
-            cp_async16(v_dst + slot + 512 * i, v_src + from, t < nv ? 16u : 0u);
+            const int t = tq + 8 * i;
+            const int64_t from = (int64_t)row * kCodeBytes + lane * 16 + (t < nv ? 512 * i : -tq * 64);
+            cp_async16(code_dst + slot + 512 * i, p.kv.k + from, t < nv ? 16u : 0u);
+            cp_async16(code_dst + slot + 1024 + 512 * i, p.kv.v + from, t < nv ? 16u : 0u);
           }
         }
         const int t = lane & 15;
-        cp_async8(s_dst + slot, s_src + (int64_t)row * kGroups - (t < nv ? 0 : t * kGroups), t < nv ? 8u : 0u);
+        cp_async8(scale_dst + slot, (lane < 16 ? p.kv.ks : p.kv.vs) + ((uint64_t)row + (t < nv ? t : 0)) * kGroups,
+                  t < nv ? 8u : 0u);
       } else if (nv > 0) {
         const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.kv.k) + (uint64_t)row * kHeadDim;
         const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.kv.v) + (uint64_t)row * kHeadDim;
@@ -357,20 +388,21 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   };
   auto issue = [&](int st, uint32_t slot) {
     if (st < n_w) {
-#pragma unroll
-      for (int h = 0; h < kStep; ++h) issue_tile(st * kStep + h, slot + h * R::kTileBytes);
+      if constexpr (kStep == 2) {
+        const uint2 r = lds64(rows_s + st * 8);
+        issue_tile(2 * st, r.x, slot);
+        issue_tile(2 * st + 1, r.y, slot + R::kTileBytes);
+      } else {
+        issue_tile(st, lds32(rows_s + st * 4), slot);
+      }
     }
     cp_async_commit();  // one group per step, empty or not
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kStages; ++i) issue(i, i * R::kStageBytes);
 
-  // Q fragments (B operand): head n = lane / 4.  sl2: the base-2 scale of the
-  // raw logits of heads ta and ta + 1.
-  uint32_t qf[8][2];
-  float sl2[2] = {p.scale_log2, p.scale_log2};
-  // 4 bit: key nibbles enter the first product as the fp16 numbers n 2^-24
-  // (bits 0..3 of a half) and n 2^-20 (bits 4..7): one AND for two, no
+  // Queries.  4 bit: key nibbles enter the first product as the fp16 numbers
+  // n 2^-24 (bits 0..3 of a half) and n 2^-20 (bits 4..7): one AND for two, no
   // conversion.  So q is fp16 too, each head scaled by a power of two to a
   // largest magnitude in [2^14, 2^15): its 8 bits are kept exactly down to
   // 2^-31 of that, and what is lost below is under fp32's own rounding.  The
@@ -379,56 +411,43 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   // ks_g sum q_g: one product of the scales with that sum in three bf16 parts
   // (24 bits), k slots 0..3 the high parts of groups 0..3, 4..7 the middle,
   // 8..11 the low ones.
+  uint32_t qf[8][2];  // bf16: B fragments, head tq
   uint32_t off_b[2] = {0u, 0u};
+  float sl2[2] = {p.scale_log2, p.scale_log2};  // base-2 scale of the raw logits of heads ta and ta + 1
+  const uint32_t q_s = smem_u32(s_q) + tq * 256 + c * 16;
   if constexpr (kInt4) {
-    uint4(&w)[4] = qw;
-    uint32_t mx = 0;
-#pragma unroll
-    for (int G = 0; G < 4; ++G) {
-      if (n >= g) w[G] = make_uint4(0u, 0u, 0u, 0u);
-      mx = max_u16x2(mx, max_u16x2(max_u16x2(w[G].x & 0x7FFF7FFFu, w[G].y & 0x7FFF7FFFu),
-                                   max_u16x2(w[G].z & 0x7FFF7FFFu, w[G].w & 0x7FFF7FFFu)));
-    }
+    uint32_t mx = max_u16x2(max_u16x2(qw.x & 0x7FFF7FFFu, qw.y & 0x7FFF7FFFu), max_u16x2(qw.z & 0x7FFF7FFFu, qw.w & 0x7FFF7FFFu));
     mx = max(mx & 0xFFFFu, mx >> 16);
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    const uint32_t e = mx >> 7;  // biased exponent of the largest magnitude
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    const uint32_t e = mx >> 7;  // biased exponent of the head's largest magnitude
     const uint32_t fe = e == 255u || mx == 0u ? 127u : min(268u - e, 254u);
     const float f = __uint_as_float(fe << 23);  // 2^(fe - 127)
-    const float undo = p.scale_log2 * __uint_as_float(min(278u - fe, 254u) << 23);  // 2^24 / f
-#pragma unroll
-    for (int j = 0; j < 2; ++j) sl2[j] = __shfl_sync(0xffffffffu, undo, 4 * (ta + j));
-    const float f4 = f * 0x1p-4f;
-#pragma unroll
-    for (int G = 0; G < 4; ++G) {
-      const uint32_t v[4] = {w[G].x, w[G].y, w[G].z, w[G].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float fi = (i & 1) ? f4 : f;
-        qf[2 * G + (i >> 1)][i & 1] = pack_f16x2(lo_f(v[i]) * fi, hi_f(v[i]) * fi);
-      }
-    }
-    float part[4];
-#pragma unroll
-    for (int G = 0; G < 4; ++G) {
-      float sum = lo_f(w[G].x) * f + hi_f(w[G].x) * f + lo_f(w[G].y) * f + hi_f(w[G].y) * f + lo_f(w[G].z) * f +
-                  hi_f(w[G].z) * f + lo_f(w[G].w) * f + hi_f(w[G].w) * f;
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      part[G] = sum * -0x1p-21f;  // -8 * 2^-24
-    }
-    const float x0 = (c & 1) ? part[2] : part[0], x1 = (c & 1) ? part[3] : part[1];
-    const uint32_t hi = pack_bf16x2(x0, x1);
-    const float m0 = x0 - lo_f(hi), m1 = x1 - hi_f(hi);
+    const float x0 = lo_f(qw.x) * f, x1 = hi_f(qw.x) * f, x4 = lo_f(qw.z) * f, x5 = hi_f(qw.z) * f;
+    const float x2 = lo_f(qw.y) * f, x3 = hi_f(qw.y) * f, x6 = lo_f(qw.w) * f, x7 = hi_f(qw.w) * f;
+    float sum = ((x0 + x1) + (x2 + x3)) + ((x4 + x5) + (x6 + x7));
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);  // over the group's 4 threads
+    const int hd = tid >> 4, x = tid & 15;  // channels 32 (x / 4) + 8 (x % 4) ..
+    *reinterpret_cast<uint4*>(s_q + hd * 64 + x * 4) =
+        make_uint4(pack_f16x2(x0, x1), pack_f16x2(x2 * 0x1p-4f, x3 * 0x1p-4f), pack_f16x2(x4, x5), pack_f16x2(x6 * 0x1p-4f, x7 * 0x1p-4f));
+    if ((x & 3) == 0) s_off[hd][x >> 2] = sum * -0x1p-21f;  // -8 * 2^-24
+    if (x == 0) s_sl2[hd] = p.scale_log2 * __uint_as_float(min(278u - fe, 254u) << 23);  // 2^24 / f
+    __syncthreads();
+    sl2[0] = s_sl2[ta];
+    sl2[1] = s_sl2[ta + 1];
+    const float p0 = s_off[tq][2 * (c & 1)], p1 = s_off[tq][2 * (c & 1) + 1];
+    const uint32_t hi = pack_bf16x2(p0, p1);
+    const float m0 = p0 - lo_f(hi), m1 = p1 - hi_f(hi);
     const uint32_t mid = pack_bf16x2(m0, m1);
     off_b[0] = c < 2 ? hi : mid;
     off_b[1] = c < 2 ? pack_bf16x2(m0 - lo_f(mid), m1 - hi_f(mid)) : 0u;
   } else {
-    const uint32_t* q32 = reinterpret_cast<const uint32_t*>(qrow);
+    const uint32_t* q32 = reinterpret_cast<const uint32_t*>(p.q + (qh0 + (tq < g ? tq : 0)) * kHeadDim);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
-      qf[kk][0] = n < g ? __ldg(q32 + kk * 8 + c) : 0u;
-      qf[kk][1] = n < g ? __ldg(q32 + kk * 8 + 4 + c) : 0u;
+      qf[kk][0] = tq < g ? __ldg(q32 + kk * 8 + c) : 0u;
+      qf[kk][1] = tq < g ? __ldg(q32 + kk * 8 + 4 + c) : 0u;
     }
   }
 
@@ -451,35 +470,36 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
     cp_async_wait<kStages - 1>();
     __syncwarp();
     int nv[kStep];
+    uint32_t part = lds32(rows_s + st * kStep * 4);
+    if constexpr (kStep == 2) part |= lds32(rows_s + st * 8 + 4);
+    part &= kPartial;
     bool some = true;
 #pragma unroll
     for (int h = 0; h < kStep; ++h) nv[h] = kTileTokens;
-    const uint32_t part = tile_partial(st * kStep) & ((1u << kStep) - 1u);
     if (part) {
       some = false;
 #pragma unroll
       for (int h = 0; h < kStep; ++h) {
-        nv[h] = tile_valid(st * kStep + h);
+        nv[h] = s_valid[warp][st * kStep + h];
         some |= nv[h] > 0;
       }
     }
     if (some) {
       const uint32_t base = ring + slot;
       float s[kStep][4], pr[kStep][4];
-      int t0, t1;  // the tokens, in a tile, of this lane's logits
       if constexpr (kInt4) {
         // the scales, each unpacked once for the warp: lane l the key scales of
         // token l / 2, groups 2 (l % 2) and the next; and group l % 4's value
-        // scales of token pair l / 4 (tokens tp, tp + 4)
-        const int tp = (it & 3) + 8 * (it >> 2);
+        // scales of a token pair of the second product's slots
+        const int tp = (tq & 3) + 8 * (tq >> 2), tp2 = tp ^ 5;  // ((tp & 3) ^ 1) + 4
         float v[kStep][2];
         const float vn = __uint_as_float(vn_bits);
         bool high = false;
 #pragma unroll
         for (int h = 0; h < kStep; ++h) {
           const uint32_t kw = lds32(base + h * R::kTileBytes + 2048 + lane * 4);
-          v[h][0] = __uint_as_float(lds16(base + h * R::kTileBytes + 2176 + tp * 8 + icol * 2) << 16);
-          v[h][1] = __uint_as_float(lds16(base + h * R::kTileBytes + 2176 + tp * 8 + 32 + icol * 2) << 16);
+          v[h][0] = __uint_as_float(lds16(base + h * R::kTileBytes + 2176 + tp * 8 + c * 2) << 16);
+          v[h][1] = __uint_as_float(lds16(base + h * R::kTileBytes + 2176 + tp2 * 8 + c * 2) << 16);
           sts64(scales + h * R::kScaleBytes + lane * 8, lo_f(kw), hi_f(kw));
           high |= !(v[h][0] < vn) || !(v[h][1] < vn);
         }
@@ -519,36 +539,38 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
         for (int h = 0; h < kStep; ++h)
           sts32(scales + h * R::kScaleBytes + 256 + lane * 4, pack_f16x2(v[h][0] * inv_vn, v[h][1] * inv_vn));
         __syncwarp();
-        t0 = ((tq & 1) << 2) | (tq >> 1);
-        t1 = t0 + 8;
+        uint4 wa[kStep], wb[kStep], sa[kStep], sb[kStep];
 #pragma unroll
         for (int h = 0; h < kStep; ++h) {
-          const uint32_t tb = base + h * R::kTileBytes;
-          const uint4 wa = lds128(tb + lane * 16), wb = lds128(tb + 512 + lane * 16);
-          const uint32_t ka[4] = {wa.x, wa.y, wa.z, wa.w}, kb[4] = {wb.x, wb.y, wb.z, wb.w};
-          const uint4 sa = lds128(scales + h * R::kScaleBytes + t0 * 16), sb = lds128(scales + h * R::kScaleBytes + t1 * 16);
-          const float fa[4] = {__uint_as_float(sa.x), __uint_as_float(sa.y), __uint_as_float(sa.z), __uint_as_float(sa.w)};
-          const float fb[4] = {__uint_as_float(sb.x), __uint_as_float(sb.y), __uint_as_float(sb.z), __uint_as_float(sb.w)};
+          const uint32_t tb = base + h * R::kTileBytes, ka = tb + t0 * 64 + ((c ^ (t0 & 2)) << 4);
+          wa[h] = lds128(ka);
+          wb[h] = lds128(ka + 512);
+          sa[h] = lds128(scales + h * R::kScaleBytes + t0 * 16);
+          sb[h] = lds128(scales + h * R::kScaleBytes + t1 * 16);
           const uint32_t ra = lds32(tb + 2048 + t0 * 8 + (c & 1) * 4), rb = lds32(tb + 2048 + t1 * 8 + (c & 1) * 4);
           s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.f;
           mma_bf16_16816(s[h], ra, rb, ra, rb, off_b[0], off_b[1]);
+        }
 #pragma unroll
-          for (int G = 0; G < 4; ++G) {
+        for (int G = 0; G < 4; ++G) {
+          const uint4 q = lds128(q_s + G * 64);
+#pragma unroll
+          for (int h = 0; h < kStep; ++h) {
+            const uint32_t ka = part_of(wa[h], G), kb = part_of(wb[h], G);
+            // the upper bytes of both halves, by the multiplier: the logic
+            // unit is the busiest here
+            const uint32_t ha = __umulhi(ka, p.two24), hb = __umulhi(kb, p.two24);
+            const float fa = __uint_as_float(part_of(sa[h], G)), fb = __uint_as_float(part_of(sb[h], G));
             float d[4] = {0.f, 0.f, 0.f, 0.f};
-            const uint32_t ha = ka[G] >> 8, hb = kb[G] >> 8;
-            mma_f16_16816(d, ka[G] & 0x000F000Fu, kb[G] & 0x000F000Fu, ka[G] & 0x00F000F0u, kb[G] & 0x00F000F0u,
-                          qf[2 * G][0], qf[2 * G][1]);
-            mma_f16_16816(d, ha & 0x000F000Fu, hb & 0x000F000Fu, ha & 0x00F000F0u, hb & 0x00F000F0u, qf[2 * G + 1][0],
-                          qf[2 * G + 1][1]);
-            s[h][0] = fmaf(fa[G], d[0], s[h][0]);
-            s[h][1] = fmaf(fa[G], d[1], s[h][1]);
-            s[h][2] = fmaf(fb[G], d[2], s[h][2]);
-            s[h][3] = fmaf(fb[G], d[3], s[h][3]);
+            mma_f16_16816(d, ka & 0x000F000Fu, kb & 0x000F000Fu, ka & 0x00F000F0u, kb & 0x00F000F0u, q.x, q.y);
+            mma_f16_16816(d, ha & 0x000F000Fu, hb & 0x000F000Fu, ha & 0x00F000F0u, hb & 0x00F000F0u, q.z, q.w);
+            s[h][0] = fmaf(fa, d[0], s[h][0]);
+            s[h][1] = fmaf(fa, d[1], s[h][1]);
+            s[h][2] = fmaf(fb, d[2], s[h][2]);
+            s[h][3] = fmaf(fb, d[3], s[h][3]);
           }
         }
       } else {
-        t0 = tq;
-        t1 = tq + 8;
         float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
         const int kr = lane & 15, khi = lane >> 4;
 #pragma unroll
@@ -577,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
         for (int h = 0; h < kStep; ++h) {
           if (nv[h] > 0) {
             const int tile = (warp + kWarps * st) * kStep + h;
-            const int64_t slot0 = (int64_t)pair * p.k * bs + (int64_t)(j0 * tpb + tile) * kTileTokens;
+            const int64_t slot0 = ((int64_t)pair * p.k << lbs) + (int64_t)((j0 << ltpb) + tile) * kTileTokens;
             float* z0 = p.z + (slot0 + t0) * g + ta;
             float* z1 = p.z + (slot0 + t1) * g + ta;
             if (ta < g) {
@@ -601,15 +623,17 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
           const uint4 va = lds128(sc + c * 16), vb = lds128(sc + 64 + c * 16);
           const uint32_t pb[4][2] = {{hmul2(p0, va.x), hmul2(p1, vb.x)}, {hmul2(p0, va.y), hmul2(p1, vb.y)},
                                      {hmul2(p0, va.z), hmul2(p1, vb.z)}, {hmul2(p0, va.w), hmul2(p1, vb.w)}};
-          // value codes: tokens c, c + 4, c + 8, c + 12; the lane's 4 channels
-          // of each group.  Two tokens' halfwords side by side, then nibbles as
-          // n 2^-24 and n 2^-20 like the keys'; 8 times the weights' sum, taken
-          // by a product with a row of ones for each group, comes off at the
-          // end (a warp's tiles are few enough for it to cost nothing).
+          // value codes: the lane's 4 channels of each group, of its 4 tokens.
+          // Two tokens' halfwords side by side; of a byte of each, the low
+          // nibbles (n 2^-24) for one channel, and both (n 2^-24 + n' 2^-20)
+          // for the next, whose sum the first channel's comes off at the end.
+          // So does 8 times the weights' sum, taken by a product with a row of
+          // ones for each group (a warp's tiles are few enough for the
+          // difference to keep its bits).
           uint2 x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int t = c + 4 * i;
+            const int t = 4 * i + ((i & 1) ? c ^ 1 : c);
             x[i] = lds64(tb + 1024 + t * 64 + (((tq >> 1) ^ (t & 2)) << 4) + (tq & 1) * 8);
           }
 #pragma unroll
@@ -617,12 +641,11 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
             const uint32_t sel = (G & 1) ? 0x7632u : 0x5410u;
             const uint32_t u01 = __byte_perm(G < 2 ? x[0].x : x[0].y, G < 2 ? x[1].x : x[1].y, sel);
             const uint32_t u23 = __byte_perm(G < 2 ? x[2].x : x[2].y, G < 2 ? x[3].x : x[3].y, sel);
-            const uint32_t h01 = u01 >> 8, h23 = u23 >> 8;
+            const uint32_t l01 = u01 & 0x00FF00FFu, l23 = u23 & 0x00FF00FFu;
+            const uint32_t h01 = __byte_perm(u01, 0u, 0x4341), h23 = __byte_perm(u23, 0u, 0x4341);
             const uint32_t one = tq == G ? 0x3C003C00u : 0u;
-            mma_f16_16816(a.o[2 * G], u01 & 0x000F000Fu, u01 & 0x00F000F0u, u23 & 0x000F000Fu, u23 & 0x00F000F0u,
-                          pb[G][0], pb[G][1]);
-            mma_f16_16816(a.o[2 * G + 1], h01 & 0x000F000Fu, h01 & 0x00F000F0u, h23 & 0x000F000Fu, h23 & 0x00F000F0u,
-                          pb[G][0], pb[G][1]);
+            mma_f16_16816(a.o[2 * G], u01 & 0x000F000Fu, l01, u23 & 0x000F000Fu, l23, pb[G][0], pb[G][1]);
+            mma_f16_16816(a.o[2 * G + 1], h01 & 0x000F000Fu, h01, h23 & 0x000F000Fu, h23, pb[G][0], pb[G][1]);
             mma_f16_16816(a.sums, one, 0u, one, 0u, pb[G][0], pb[G][1]);
           }
         }
@@ -669,22 +692,20 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   {
     float* w0 = comb + ((warp * kMaxGroup) + ta) * kRowPad;
     if constexpr (kInt4) {
-      // o[2G + e][i]: channel 32 G + 4 tq + 2 e + (i / 2), head ta + (i & 1);
-      // the weights' sums of group G sit in the lanes of row G
-      uint32_t nans = __ballot_sync(0xffffffffu, v_nan);  // bit l: group l % 4
-      nans |= nans >> 16;
-      nans |= nans >> 8;
-      nans |= nans >> 4;
+      // o[2G + e][i]: channels 32 G + 4 tq + 2 e (and, with it, the next), head
+      // ta + (i & 1); the weights' sums of group G sit in the lanes of row G
+      const uint32_t nans = __ballot_sync(0xffffffffu, v_nan);  // lanes l = c (mod 4): group c
+      const float mine = (nans & (0x11111111u << c)) ? __int_as_float(0x7FFFFFFF) : __uint_as_float(vn_bits);
 #pragma unroll
-      for (int dm = 0; dm < 8; ++dm) {
-        const int d = (dm >> 1) * 32 + 4 * tq + 2 * (dm & 1);
-        float vn = __uint_as_float(__shfl_sync(0xffffffffu, vn_bits, dm >> 1));
-        if ((nans >> (dm >> 1)) & 1u) vn = __int_as_float(0x7FFFFFFF);
+      for (int G = 0; G < 4; ++G) {
+        const float vn = __shfl_sync(0xffffffffu, mine, G);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float off = -8.f * __shfl_sync(0xffffffffu, a.sums[j], (dm >> 1) * 4 + c);
-          w0[j * kRowPad + d] = fmaf(a.o[dm][j], 0x1p24f, off) * vn;
-          w0[j * kRowPad + d + 1] = fmaf(a.o[dm][2 + j], 0x1p20f, off) * vn;
+          const float off = -8.f * __shfl_sync(0xffffffffu, a.sums[j], G * 4 + c);
+          const float x0 = a.o[2 * G][j] * 0x1p24f, x2 = a.o[2 * G + 1][j] * 0x1p24f;
+          const float x1 = fmaf(a.o[2 * G][2 + j], 0x1p20f, x0 * -0x1p-4f), x3 = fmaf(a.o[2 * G + 1][2 + j], 0x1p20f, x2 * -0x1p-4f);
+          *reinterpret_cast<float4*>(w0 + j * kRowPad + 32 * G + 4 * tq) =
+              make_float4((x0 + off) * vn, (x1 + off) * vn, (x2 + off) * vn, (x3 + off) * vn);
         }
       }
     } else {
@@ -705,6 +726,12 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
     s_l[warp][2 * lane + 1] = a.l[1];
   }
   __syncthreads();
+  auto write_lse = [&](int j, float den, float M) {
+    const float l2 = den == 0.f ? kNegInf : M + log2f(den);
+    if (p.lse) p.lse[qh0 + j] = l2 * 0.6931471805599453f;
+    if (kAcc) p.lse2[qh0 + j] = l2;
+    s_inv[j] = den == 0.f ? 0.f : __frcp_rn(den);
+  };
   if (tid < g) {  // per head: the maximum over the warps, each warp's weight, the sum
     const int j = tid;
     float M = kNegInf;
@@ -720,26 +747,22 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
     }
     s_cm[j] = M;
     s_cden[j] = den;
+    if (nchunks == 1) write_lse(j, den, M);
   }
   __syncthreads();
-  const int d = tid;
-  auto combined = [&](int j) {
+  auto combined = [&](int j, int d) {
     float num = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) num += s_ww[w][j] * comb[(w * kMaxGroup + j) * kRowPad + d];
     return num;
   };
-  auto finish = [&](int j, float num, float den, float M) {
-    p.out[(qh0 + j) * kHeadDim + d] = __float2bfloat16_rn(den == 0.f ? 0.f : num / den);
-    if (d == 0) {
-      const float l2 = den == 0.f ? kNegInf : M + log2f(den);
-      if (p.lse) p.lse[qh0 + j] = l2 * 0.6931471805599453f;
-      if (kAcc) p.lse2[qh0 + j] = l2;
-    }
-  };
+  auto finish = [&](int j, int d, float num) { p.out[(qh0 + j) * kHeadDim + d] = __float2bfloat16_rn(num * s_inv[j]); };
   if (nchunks == 1) {
-#pragma unroll 1
-    for (int j = 0; j < g; ++j) finish(j, combined(j), s_cden[j], s_cm[j]);
+#pragma unroll 2
+    for (int j = 0; j < g; ++j) {
+#pragma unroll
+      for (int i = 0; i < kDims; ++i) finish(j, tid + kThreads * i, combined(j, tid + kThreads * i));
+    }
     __syncthreads();  // the next pair's ring takes the combine area
     continue;
   }
@@ -748,8 +771,9 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   float* part = p.partials + ((int64_t)pair * p.max_chunks + chunk) * g * kPartStride;
 #pragma unroll 1
   for (int j = 0; j < g; ++j) {
-    part[j * kPartStride + d] = combined(j);
-    if (d == 0) {
+#pragma unroll
+    for (int i = 0; i < kDims; ++i) part[j * kPartStride + tid + kThreads * i] = combined(j, tid + kThreads * i);
+    if (tid == 0) {
       part[j * kPartStride + kHeadDim] = s_cm[j];
       part[j * kPartStride + kHeadDim + 1] = s_cden[j];
     }
@@ -769,9 +793,12 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   const float4* src4 = reinterpret_cast<const float4*>(p.partials + (int64_t)pair * p.max_chunks * rec);
   const float* stage = reinterpret_cast<const float*>(smem);
   const uint32_t stage_s = smem_u32(smem);
-  float num[kMaxGroup];
+  float num[kMaxGroup][kDims];
 #pragma unroll
-  for (int j = 0; j < kMaxGroup; ++j) num[j] = 0.f;
+  for (int j = 0; j < kMaxGroup; ++j) {
+#pragma unroll
+    for (int i = 0; i < kDims; ++i) num[j][i] = 0.f;
+  }
   if (tid < g) {
     s_mr[tid] = kNegInf;
     s_den[tid] = 0.f;
@@ -806,20 +833,33 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kMaxGroup; ++j)
-      if (j < g) num[j] *= s_a[j];
+    for (int j = 0; j < kMaxGroup; ++j) {
+      if (j < g) {
+#pragma unroll
+        for (int i = 0; i < kDims; ++i) num[j][i] *= s_a[j];
+      }
+    }
 #pragma unroll 2
     for (int cc = 0; cc < nbat; ++cc) {
-      const float* rc = stage + cc * g * kPartStride + d;
+      const float* rc = stage + cc * g * kPartStride + tid;
 #pragma unroll
-      for (int j = 0; j < kMaxGroup; ++j)
-        if (j < g) num[j] += s_w[cc * g + j] * rc[j * kPartStride];
+      for (int j = 0; j < kMaxGroup; ++j) {
+        if (j < g) {
+#pragma unroll
+          for (int i = 0; i < kDims; ++i) num[j][i] += s_w[cc * g + j] * rc[j * kPartStride + kThreads * i];
+        }
+      }
     }
     __syncthreads();  // the next batch overwrites the staging area and the weights
   }
+  if (tid < g) write_lse(tid, s_den[tid], s_mr[tid]);
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < kMaxGroup; ++j)
-    if (j < g) finish(j, num[j], s_den[j], s_mr[j]);
+    if (j < g) {
+#pragma unroll
+      for (int i = 0; i < kDims; ++i) finish(j, tid + kThreads * i, num[j][i]);
+    }
   }
 }
 
@@ -830,27 +870,29 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
 __global__ void __launch_bounds__(256) kv_weights_kernel(KvAttnParams p) {
   pdl_wait();
   pdl_trigger_early();
-  const int per = p.k * p.bs;
-  const int ctas = (per + 255) / 256;  // per pair
-  const int64_t pair = blockIdx.x / ctas;
-  const int i = (int)(blockIdx.x - pair * ctas) * 256 + threadIdx.x;
-  if (i >= per) return;
-  const int b = (int)(pair / p.Hkv), h = (int)(pair - (int64_t)b * p.Hkv);
+  const int lbs = 31 - __clz(p.bs);
+  const int ctas = ((p.k << lbs) + 255) >> 8;  // per pair
+  const int pair = blockIdx.x / ctas;
+  const int i = (blockIdx.x - pair * ctas) * 256 + threadIdx.x, j = i >> lbs;
+  const int b = pair / p.Hkv, h = pair - b * p.Hkv;
+  int blk = j;
+  if (p.sel_idx && j < p.k) blk = __ldg(p.sel_idx + (int64_t)pair * p.k_row + j);
   const int L = __ldg(p.seq_lens + b);
-  if (L < 1 || L > p.kv.Lcap) return;
-  const int nb = (L + p.bs - 1) / p.bs;
-  const int j = i / p.bs;
-  const int cnt = p.sel_idx ? __ldg(p.sel_cnt + pair) : nb;
-  if (j >= cnt) return;
-  const int blk = p.sel_idx ? __ldg(p.sel_idx + pair * p.k_row + j) : j;
-  const int t = blk * p.bs + (i - j * p.bs);
-  if (blk < 0 || blk >= nb || t >= L) return;
-  if (kv_row(p.kv.pages, b, h, p.Hkv, p.kv.Lcap, p.bs, t) < 0) return;  // a bad page: nothing was attended
-  const float* z = p.z + (pair * per + i) * p.g;
+  const int cnt = p.sel_idx ? __ldg(p.sel_cnt + pair) : p.k;
+  if (j >= min(cnt, p.k) || L < 1 || L > p.kv.Lcap) return;
+  const int t = (blk << lbs) + (i & (p.bs - 1));
+  if (blk < 0 || blk >= (L + p.bs - 1) >> lbs || t >= L) return;
+  if (p.kv.pages.table) {  // a bad page: nothing was attended
+    const int page = __ldg(p.kv.pages.table + (int64_t)b * p.kv.pages.max_blocks + blk);
+    if (page < 0 || page >= p.kv.pages.num_pages) return;
+  }
+  const float* z = p.z + (((int64_t)pair * p.k << lbs) + i) * p.g;
   const float* l = p.lse2 + (int64_t)b * p.Hq + (int64_t)h * p.g;
   float w = 0.f;
-  for (int q = 0; q < p.g; ++q) w += exp2f(z[q] - l[q]);
-  atomicAdd(p.acc + pair * p.kv.Lcap + t, w);
+#pragma unroll
+  for (int q = 0; q < kMaxGroup; ++q)
+    if (q < p.g) w += exp2f(__ldcg(z + q) - __ldcg(l + q));
+  atomicAdd(p.acc + (int64_t)pair * p.kv.Lcap + t, w);
 }
 
 template <bool kInt4, bool kAcc>
