@@ -661,11 +661,12 @@ struct KvSplit {
 };
 
 // Chosen by an estimate in microseconds, from timings of 4-bit caches (bf16
-// tiles take three times as long, which leaves the order as it is): a CTA
-// spends 4.5 on a range, 2.5 more where ranges of a pair are merged, and 0.12
-// a tile alone, 0.064 times the SM's CTAs when they share it.  Against even
-// ranges over the pairs' borders, 256 pairs of 32, 128 and 256 tiles took 8.7,
-// 20.6 and 38.0 with one range each and 17.7, 28.4 and 41.9 without.
+// tiles take two and a half times as long, which leaves the order as it is):
+// a range takes 4, or 5 where ranges of a pair are merged, and a tile 0.109,
+// 0.149 or 0.216 with one, two or three CTAs on an SM.  256 pairs of 256
+// tiles: 42.5 with one range each, 52.9 with two, 41.8 with even ranges over
+// the pairs' borders; 256 pairs of 32 tiles: 8.7 with one range each, 17.7
+// with even ranges.
 KvSplit kv_split(const kin_dims& d, int k, bool dense) {
   const int tpb = d.block_size / kTileTokens;
   const int64_t pairs = pairs_of(d);
@@ -673,8 +674,7 @@ KvSplit kv_split(const kin_dims& d, int k, bool dense) {
   const int least = (8 + tpb - 1) / tpb;                             // a step of each warp
   const int64_t wave = (int64_t)kTargetSMs * kKvCtasPerSm;
   auto range_us = [&](int64_t tiles, int64_t per_sm, bool merged) {
-    const double shared = 0.064 * (double)per_sm;
-    return (double)tiles * (shared > 0.12 ? shared : 0.12) + (merged ? 7.0 : 4.5);
+    return (double)tiles * (per_sm <= 1 ? 0.109 : per_sm == 2 ? 0.149 : 0.216) + (merged ? 5.0 : 4.0);
   };
   KvSplit best{0, 0};
   double best_us = 0;
@@ -694,7 +694,7 @@ KvSplit kv_split(const kin_dims& d, int k, bool dense) {
   const int64_t waves = (slots + wave * most - 1) / (wave * most);
   const int64_t per = (slots + wave * waves - 1) / (wave * waves);
   if (!dense && per >= least && per < k) {
-    const double us = (double)waves * (range_us(per * tpb, kKvCtasPerSm, true) + 7.0);
+    const double us = (double)waves * (range_us(per * tpb, kKvCtasPerSm, true) + 5.0);
     if (us < best_us) best = KvSplit{(int)per, k};
   }
   return best;

@@ -71,6 +71,25 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D = A B, from zero
+__device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ void mma_bf16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -234,7 +253,9 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = p.g, bs = p.bs, Lcap = p.kv.Lcap;
   pdl_wait();  // the selection comes from the select kernels
-  pdl_trigger_early();
+  // No early launch_dependents: the next grid's CTAs would take what room this
+  // one leaves on each SM and so lie unevenly (296 CTAs of 128 tiles, launched
+  // back to back: 29.5 us a call with it, 23.4 without).
   const int lbs = 31 - __clz(bs), ltpb = lbs - 4;  // log2 of a block's tokens and of its tiles
   const int c = lane & 3, tq = lane >> 2, ta = 2 * c;
 
@@ -548,8 +569,7 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
           sa[h] = lds128(scales + h * R::kScaleBytes + t0 * 16);
           sb[h] = lds128(scales + h * R::kScaleBytes + t1 * 16);
           const uint32_t ra = lds32(tb + 2048 + t0 * 8 + (c & 1) * 4), rb = lds32(tb + 2048 + t1 * 8 + (c & 1) * 4);
-          s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.f;
-          mma_bf16_16816(s[h], ra, rb, ra, rb, off_b[0], off_b[1]);
+          mma_bf16_new(s[h], ra, rb, ra, rb, off_b[0], off_b[1]);
         }
 #pragma unroll
         for (int G = 0; G < 4; ++G) {
@@ -561,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
             // unit is the busiest here
             const uint32_t ha = __umulhi(ka, p.two24), hb = __umulhi(kb, p.two24);
             const float fa = __uint_as_float(part_of(sa[h], G)), fb = __uint_as_float(part_of(sb[h], G));
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16_16816(d, ka & 0x000F000Fu, kb & 0x000F000Fu, ka & 0x00F000F0u, kb & 0x00F000F0u, q.x, q.y);
+            float d[4];
+            mma_f16_new(d, ka & 0x000F000Fu, kb & 0x000F000Fu, ka & 0x00F000F0u, kb & 0x00F000F0u, q.x, q.y);
             mma_f16_16816(d, ha & 0x000F000Fu, hb & 0x000F000Fu, ha & 0x00F000F0u, hb & 0x00F000F0u, q.z, q.w);
             s[h][0] = fmaf(fa, d[0], s[h][0]);
             s[h][1] = fmaf(fa, d[1], s[h][1]);
