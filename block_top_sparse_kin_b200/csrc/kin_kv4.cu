@@ -31,68 +31,89 @@ constexpr int kKvWarps = kKvThreads / 32;
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // 8 channels of a group in 4 bits: w = the bf16 pairs of this lane.  Returns
-// the scale's bits (the same in the group's 4 lanes) and the nibbles n[i] =
-// c_i + 8 in the low bits of n.
+// the scale's bits (the same in the group's 4 lanes) and the codes c[i] as
+// numbers.
 //
-// The rounding is exact with one reciprocal: x has an 8-bit significand and
-// a midpoint (c + 1/2) s a 12-bit one, so an x that is not at a midpoint is
-// at least 2^-12 away from it, relative to it; x * (1/s) is within 2^-22,
-// and rounding it to 16 significant bits moves a quotient at a midpoint onto
-// it and no other across one.
-__device__ __forceinline__ uint32_t encode8(const uint4& w, uint32_t (&n)[8]) {
+// The rounding is exact with one reciprocal.  x has an 8-bit significand S
+// and a midpoint (c + 1/2) s a product of an odd number 2c + 1 <= 13 and an
+// 8-bit one, so a quotient x / s that is not a midpoint is at least 2^-11
+// away from one (2^-8 of 1/2, 2^-10 of 3/2, 2^-11 of 5/2 and 7/2, 2^-12 of
+// 9/2 to 13/2).  x times the rounded reciprocal, added to 1.5 * 2^11 in one
+// rounding, is the quotient to 2^-13 + 2^-21 on a grid of 2^-12: at a midpoint
+// exactly there, elsewhere on its side of it.  The second addition rounds
+// that to a whole number, half to even, and the third leaves it.  A normal
+// scale is a / 7 to 2^-9, so no quotient reaches 7.5.
+__device__ __forceinline__ uint32_t encode8(const uint4& w, float (&c)[8]) {
   const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max(v[i] & 0x7FFFu, (v[i] >> 16) & 0x7FFFu));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  uint32_t m = max_u16x2(max_u16x2(v[0] & 0x7FFF7FFFu, v[1] & 0x7FFF7FFFu), max_u16x2(v[2] & 0x7FFF7FFFu, v[3] & 0x7FFF7FFFu));
+  m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  m = max(m & 0xFFFFu, m >> 16);
   // a NaN's bits are above infinity's, so the integer maximum keeps it
-  const bool finite = m < 0x7F80u;
-  const float a = __uint_as_float(m << 16);
-  const uint32_t s = finite ? (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(a, 7.0f))) : 0x7FC0u;
+  const uint32_t s = m < 0x7F80u ? (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(__uint_as_float(m << 16), 7.0f)))
+                                 : 0x7FC0u;
   const float sf = __uint_as_float(s << 16);
-  // 1 / s overflows below 2^-126: there x and s are first scaled by 2^100 (exact)
-  const float up = sf < 0x1p-100f ? 0x1p100f : 1.0f;
-  const bool any = finite && sf > 0.f;
-  const float inv = any ? __frcp_rn(sf * up) : 0.f;
+  constexpr float kGrid = 0x1.8p11f, kWhole = 0x1.8p23f - 0x1.8p11f;
+  if (sf >= 0x1p-100f) {
+    const float inv = __frcp_rn(sf);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float x = any ? ((i & 1) ? bf16_hi(v[i >> 1]) : bf16_lo(v[i >> 1])) : 0.f;
-    float y = (x * up) * inv;
-    y = __uint_as_float((__float_as_uint(y) + 0x80u) & 0xFFFFFF00u);
-    y = fminf(fmaxf(y, -7.f), 7.f);
-    // 1.5 * 2^23 + 8: the sum's low bits are the rounded y + 8
-    n[i] = __float_as_uint(__fadd_rn(y, 12582920.0f)) & 15u;
+    for (int i = 0; i < 8; ++i) {
+      const float x = (i & 1) ? bf16_hi(v[i >> 1]) : bf16_lo(v[i >> 1]);
+      c[i] = __fsub_rn(__fadd_rn(__fmaf_rn(x, inv, kGrid), kWhole), 12582912.f);
+    }
+  } else {
+    // a scale of zero, or NaN: every code is 0.  A tiny one: x and s are first
+    // scaled by 2^100 (exact), since 1 / s overflows below 2^-126; a subnormal
+    // scale may be rounded by half, so the quotient is cut at 7.
+    const bool some = sf > 0.f;
+    const float inv = some ? __frcp_rn(sf * 0x1p100f) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = some ? ((i & 1) ? bf16_hi(v[i >> 1]) : bf16_lo(v[i >> 1])) * 0x1p100f : 0.f;
+      const float y = fminf(fmaxf(x * inv, -7.f), 7.f);
+      c[i] = __fsub_rn(__fadd_rn(__fadd_rn(y, kGrid), kWhole), 12582912.f);
+    }
   }
   return s;
 }
 
-__device__ __forceinline__ uint32_t pack_key(const uint32_t (&n)[8]) {
-  return (n[0] | (n[2] << 4) | (n[4] << 8) | (n[6] << 12)) | ((n[1] | (n[3] << 4) | (n[5] << 8) | (n[7] << 12)) << 16);
+// Four codes as the nibbles c + 8 of the low half of a word: the number
+// sum 16^i (c_i + 8) < 2^16, exact, read off behind 2^23.
+__device__ __forceinline__ uint32_t nibbles4(float c0, float c1, float c2, float c3) {
+  const float n = fmaf(fmaf(fmaf(c3, 16.f, c2), 16.f, c1), 16.f, c0);
+  return __float_as_uint(n + (8388608.f + 34952.f));  // 8 * 0x1111
+}
+
+// Nibble i of w as a number: behind 2^23, less 2^23 and the offset.
+__device__ __forceinline__ float code_of(uint32_t w, int i) {
+  return __uint_as_float(((w >> (4 * i)) & 15u) | 0x4B000000u) - 8388616.f;
 }
 
 // Values of a key word: channel e of the word times s.
 __device__ __forceinline__ void key_values(uint32_t w, float s, float (&x)[8]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int nib = (e >> 1) + 4 * (e & 1);
-    x[e] = ((float)((w >> (4 * nib)) & 15u) - 8.0f) * s;
-  }
+  for (int e = 0; e < 8; ++e) x[e] = code_of(w, (e >> 1) + 4 * (e & 1)) * s;
 }
 
 // Lane x of a half holds 8 channels 32g + 8c ..: g = x / 4, c = x % 4.
 // Writes a row's codes and scales; half 0 a key row, half 1 a value row.
-__device__ __forceinline__ void write_row(const KvView& kv, int half, int x, int64_t row, const uint32_t (&n)[8],
-                                          uint32_t s) {
+__device__ __forceinline__ void write_row(const KvView& kv, int half, int x, int64_t row, const float (&n)[8], uint32_t s) {
   const int g = x >> 2, c = x & 3;
   if (half == 0) {
-    *reinterpret_cast<uint32_t*>(kv.k + row * kCodeBytes + (4 * c + g) * 4) = pack_key(n);
+    *reinterpret_cast<uint32_t*>(kv.k + row * kCodeBytes + (4 * c + g) * 4) =
+        __byte_perm(nibbles4(n[0], n[2], n[4], n[6]), nibbles4(n[1], n[3], n[5], n[7]), 0x5410);
     if (c == 0) kv.ks[row * kGroups + g] = (uint16_t)s;
   } else {
     uint16_t* o = reinterpret_cast<uint16_t*>(kv.v + row * kCodeBytes);
-    o[8 * c + g] = (uint16_t)(n[0] | (n[1] << 4) | (n[2] << 8) | (n[3] << 12));
-    o[8 * c + 4 + g] = (uint16_t)(n[4] | (n[5] << 4) | (n[6] << 8) | (n[7] << 12));
+    o[8 * c + g] = (uint16_t)nibbles4(n[0], n[1], n[2], n[3]);
+    o[8 * c + 4 + g] = (uint16_t)nibbles4(n[4], n[5], n[6], n[7]);
     if (c == 0) kv.vs[row * kGroups + g] = (uint16_t)s;
   }
 }
@@ -188,12 +209,12 @@ __global__ void __launch_bounds__(kKvThreads) kv4_write_kernel(Kv4WriteParams p)
 #pragma unroll
     for (int u = 0; u < kWriteRows; ++u) {
       if (t + u < t1) {  // warp-uniform
-        uint32_t n[8];
+        float n[8];
         const uint32_t s = encode8(w[u], n);
         write_row(p.dst, half, x, row0 + (t + u - t0), n, s);
         const float sf = __uint_as_float(s << 16);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += ((float)n[e] - 8.0f) * sf;
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(n[e], sf, acc[e]);  // the product is exact
       }
     }
   }
@@ -276,7 +297,7 @@ __global__ void __launch_bounds__(kKvThreads) kv4_load_kernel(Kv4LoadParams p) {
         key_values(w[u], sf, v);
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = ((float)((w[u] >> (4 * e)) & 15u) - 8.0f) * sf;
+        for (int e = 0; e < 8; ++e) v[e] = code_of(w[u], e) * sf;
       }
       // the product has up to 11 significant bits: one rounding to bf16
       uint4 o;

@@ -622,13 +622,20 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
             const int64_t slot0 = ((int64_t)pair * p.k << lbs) + (int64_t)((j0 << ltpb) + tile) * kTileTokens;
             float* z0 = p.z + (slot0 + t0) * g + ta;
             float* z1 = p.z + (slot0 + t1) * g + ta;
-            if (ta < g) {
-              z0[0] = s[h][0] * sl2[0];
-              z1[0] = s[h][2] * sl2[0];
-            }
-            if (ta + 1 < g) {
-              z0[1] = s[h][1] * sl2[1];
-              z1[1] = s[h][3] * sl2[1];
+            if (!(g & 1)) {
+              if (ta < g) {
+                *reinterpret_cast<float2*>(z0) = make_float2(s[h][0] * sl2[0], s[h][1] * sl2[1]);
+                *reinterpret_cast<float2*>(z1) = make_float2(s[h][2] * sl2[0], s[h][3] * sl2[1]);
+              }
+            } else {
+              if (ta < g) {
+                z0[0] = s[h][0] * sl2[0];
+                z1[0] = s[h][2] * sl2[0];
+              }
+              if (ta + 1 < g) {
+                z0[1] = s[h][1] * sl2[1];
+                z1[1] = s[h][3] * sl2[1];
+              }
             }
           }
         }
@@ -884,35 +891,64 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
 }
 
 // The weights of the attended tokens, once every lse is known: one thread per
-// (pair, slot of the kept blocks) adds sum_j 2^(z_j - lse2_j) to its token's
-// running sum.  Each kept token has one slot, so the addition is an atomic
-// only where an index is listed twice (it then counts twice).
+// four consecutive tokens of a kept block adds sum_j 2^(z_j - lse2_j) to each
+// one's running sum.  A kept token has one slot, so the addition is an atomic
+// only where a block is listed twice (it then counts twice).  The logits come
+// from L2; four tokens a thread keep one wave's worth of them in flight.
+template <int G>
 __global__ void __launch_bounds__(256) kv_weights_kernel(KvAttnParams p) {
   pdl_wait();
-  pdl_trigger_early();
-  const int lbs = 31 - __clz(p.bs);
-  const int ctas = ((p.k << lbs) + 255) >> 8;  // per pair
+  const int lbs = 31 - __clz(p.bs), quads = p.k << (lbs - 2);  // of a pair
+  const int ctas = (quads + 255) >> 8;
   const int pair = blockIdx.x / ctas;
-  const int i = (blockIdx.x - pair * ctas) * 256 + threadIdx.x, j = i >> lbs;
+  const int i = (blockIdx.x - pair * ctas) * 256 + threadIdx.x, j = i >> (lbs - 2);
   const int b = pair / p.Hkv, h = pair - b * p.Hkv;
-  int blk = j;
-  if (p.sel_idx && j < p.k) blk = __ldg(p.sel_idx + (int64_t)pair * p.k_row + j);
+  if (j >= p.k) return;
+  const int blk = p.sel_idx ? __ldg(p.sel_idx + (int64_t)pair * p.k_row + j) : j;
   const int L = __ldg(p.seq_lens + b);
   const int cnt = p.sel_idx ? __ldg(p.sel_cnt + pair) : p.k;
-  if (j >= min(cnt, p.k) || L < 1 || L > p.kv.Lcap) return;
-  const int t = (blk << lbs) + (i & (p.bs - 1));
-  if (blk < 0 || blk >= (L + p.bs - 1) >> lbs || t >= L) return;
+  float z[4 * G], l[G];
+  const float4* z4 = reinterpret_cast<const float4*>(p.z + (((int64_t)pair * p.k << lbs) + 4 * (int64_t)i) * G);
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const float4 v = __ldcg(z4 + q);
+    z[4 * q] = v.x;
+    z[4 * q + 1] = v.y;
+    z[4 * q + 2] = v.z;
+    z[4 * q + 3] = v.w;
+    l[q] = __ldcg(p.lse2 + (int64_t)b * p.Hq + (int64_t)h * G + q);
+  }
+  if (j >= cnt || L < 1 || L > p.kv.Lcap || blk < 0 || blk >= (L + p.bs - 1) >> lbs) return;
   if (p.kv.pages.table) {  // a bad page: nothing was attended
     const int page = __ldg(p.kv.pages.table + (int64_t)b * p.kv.pages.max_blocks + blk);
     if (page < 0 || page >= p.kv.pages.num_pages) return;
   }
-  const float* z = p.z + (((int64_t)pair * p.k << lbs) + i) * p.g;
-  const float* l = p.lse2 + (int64_t)b * p.Hq + (int64_t)h * p.g;
-  float w = 0.f;
+  const int t0 = (blk << lbs) + ((4 * i) & (p.bs - 1));
+  float* acc = p.acc + (int64_t)pair * p.kv.Lcap + t0;
 #pragma unroll
-  for (int q = 0; q < kMaxGroup; ++q)
-    if (q < p.g) w += exp2f(__ldcg(z + q) - __ldcg(l + q));
-  atomicAdd(p.acc + (int64_t)pair * p.kv.Lcap + t, w);
+  for (int u = 0; u < 4; ++u) {
+    if (t0 + u < L) {
+      float w = 0.f;
+#pragma unroll
+      for (int q = 0; q < G; ++q) w += exp2f(z[u * G + q] - l[q]);
+      atomicAdd(acc + u, w);
+    }
+  }
+}
+
+static cudaError_t launch_kv_weights(const KvAttnParams& p, cudaStream_t s) {
+  const int64_t quads = (int64_t)p.k * p.bs / 4;
+  const dim3 grid((unsigned)((int64_t)p.B * p.Hkv * ((quads + 255) / 256))), block(256);
+  switch (p.g) {
+    case 1: return launch_pdl(kv_weights_kernel<1>, grid, block, 0, s, p);
+    case 2: return launch_pdl(kv_weights_kernel<2>, grid, block, 0, s, p);
+    case 3: return launch_pdl(kv_weights_kernel<3>, grid, block, 0, s, p);
+    case 4: return launch_pdl(kv_weights_kernel<4>, grid, block, 0, s, p);
+    case 5: return launch_pdl(kv_weights_kernel<5>, grid, block, 0, s, p);
+    case 6: return launch_pdl(kv_weights_kernel<6>, grid, block, 0, s, p);
+    case 7: return launch_pdl(kv_weights_kernel<7>, grid, block, 0, s, p);
+    default: return launch_pdl(kv_weights_kernel<8>, grid, block, 0, s, p);
+  }
 }
 
 template <bool kInt4, bool kAcc>
@@ -920,11 +956,8 @@ static cudaError_t launch_kv_attn_as(const KvAttnParams& p, cudaStream_t s) {
   const auto kernel = kv_attn_kernel<kInt4, kAcc>;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), 16 + 2 * kInt4 + kAcc, Ring<kInt4>::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t pairs = (int64_t)p.B * p.Hkv;
   e = launch_pdl(kernel, dim3((unsigned)((p.slots + p.per - 1) / p.per)), dim3(kThreads), Ring<kInt4>::kSmem, s, p);
-  if (e != cudaSuccess || !kAcc) return e;
-  const int64_t per = (int64_t)p.k * p.bs;
-  return launch_pdl(kv_weights_kernel, dim3((unsigned)(pairs * ((per + 255) / 256))), dim3(256), 0, s, p);
+  return e != cudaSuccess || !kAcc ? e : launch_kv_weights(p, s);
 }
 
 cudaError_t launch_kv_attn(const KvAttnParams& p, cudaStream_t s) {
