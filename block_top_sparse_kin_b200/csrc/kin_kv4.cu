@@ -15,10 +15,12 @@
 // nibbles 0..3, odd ones in 4..7); a value row is 32 halfwords, halfword
 // 4r + g holding channels 32g + 4r .. + 3.
 //
-// Layout of the work: one warp per block (16 to 128 tokens); its lower half
-// holds the key row, its upper half the value row, lane x of a half 8
-// channels (one 16-byte load of bf16), so a group is 4 lanes and its maximum
-// two shuffles.  Both are streams bounded by HBM.
+// Layout of the work: half a warp holds a row, lane x of it 8 channels (one
+// 16-byte load of bf16), so a group is 4 lanes and its maximum two shuffles.
+// A warp has keys or values, never both (their orders would cost it both
+// paths), and to store, two consecutive blocks, one each half: a lane adds up
+// its 8 channels of a block's mean on the way.  All are streams bounded by
+// HBM; what they spend per row decides how near they come.
 #include "kin_internal.cuh"
 
 namespace kin {
@@ -37,6 +39,12 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // 8 channels of a group in 4 bits: w = the bf16 pairs of this lane.  Returns
 // the scale's bits (the same in the group's 4 lanes) and the codes c[i] as
 // numbers.
@@ -49,7 +57,9 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 // rounding, is the quotient to 2^-13 + 2^-21 on a grid of 2^-12: at a midpoint
 // exactly there, elsewhere on its side of it.  The second addition rounds
 // that to a whole number, half to even, and the third leaves it.  A normal
-// scale is a / 7 to 2^-9, so no quotient reaches 7.5.
+// scale is a / 7 to 2^-9, so no quotient reaches 7.5.  The scale itself: a / 7
+// is never a midpoint of bf16 (7 times an odd 9-bit number has 11 bits, a has
+// 8) and at least 2^-12 away from one, so a times the rounded 1 / 7 serves.
 __device__ __forceinline__ uint32_t encode8(const uint4& w, float (&c)[8]) {
   const uint32_t v[4] = {w.x, w.y, w.z, w.w};
   uint32_t m = max_u16x2(max_u16x2(v[0] & 0x7FFF7FFFu, v[1] & 0x7FFF7FFFu), max_u16x2(v[2] & 0x7FFF7FFFu, v[3] & 0x7FFF7FFFu));
@@ -57,12 +67,12 @@ __device__ __forceinline__ uint32_t encode8(const uint4& w, float (&c)[8]) {
   m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
   m = max(m & 0xFFFFu, m >> 16);
   // a NaN's bits are above infinity's, so the integer maximum keeps it
-  const uint32_t s = m < 0x7F80u ? (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(__uint_as_float(m << 16), 7.0f)))
+  const uint32_t s = m < 0x7F80u ? (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(m << 16) * 0x1.24924ap-3f))
                                  : 0x7FC0u;
   const float sf = __uint_as_float(s << 16);
   constexpr float kGrid = 0x1.8p11f, kWhole = 0x1.8p23f - 0x1.8p11f;
   if (sf >= 0x1p-100f) {
-    const float inv = __frcp_rn(sf);
+    const float inv = rcp_approx(sf);  // to 2^-23
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float x = (i & 1) ? bf16_hi(v[i >> 1]) : bf16_lo(v[i >> 1]);
@@ -102,33 +112,17 @@ __device__ __forceinline__ void key_values(uint32_t w, float s, float (&x)[8]) {
   for (int e = 0; e < 8; ++e) x[e] = code_of(w, (e >> 1) + 4 * (e & 1)) * s;
 }
 
-// Lane x of a half holds 8 channels 32g + 8c ..: g = x / 4, c = x % 4.
-// Writes a row's codes and scales; half 0 a key row, half 1 a value row.
-__device__ __forceinline__ void write_row(const KvView& kv, int half, int x, int64_t row, const float (&n)[8], uint32_t s) {
-  const int g = x >> 2, c = x & 3;
-  if (half == 0) {
-    *reinterpret_cast<uint32_t*>(kv.k + row * kCodeBytes + (4 * c + g) * 4) =
-        __byte_perm(nibbles4(n[0], n[2], n[4], n[6]), nibbles4(n[1], n[3], n[5], n[7]), 0x5410);
-    if (c == 0) kv.ks[row * kGroups + g] = (uint16_t)s;
-  } else {
-    uint16_t* o = reinterpret_cast<uint16_t*>(kv.v + row * kCodeBytes);
-    o[8 * c + g] = (uint16_t)nibbles4(n[0], n[1], n[2], n[3]);
-    o[8 * c + 4 + g] = (uint16_t)nibbles4(n[4], n[5], n[6], n[7]);
-    if (c == 0) kv.vs[row * kGroups + g] = (uint16_t)s;
-  }
-}
-
 }  // namespace
 
-// The key half's block sum as a mean row: lane l of the warp takes channels
-// 4l .. 4l + 3 from lane l / 2 and stores them in the layout the flag names.
-__device__ __forceinline__ void store_half_mean(void* means, int flag, int64_t rows, int64_t row, int lane,
+// A block's mean row from the half warp `half` that holds its sums: lane l of
+// the warp takes channels 4l .. 4l + 3 from lane l / 2 of that half.
+__device__ __forceinline__ void store_half_mean(void* means, int flag, int64_t rows, int64_t row, int lane, int half,
                                                 const float (&acc)[8], float count) {
   float m[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float lo = __shfl_sync(0xffffffffu, acc[i], lane >> 1);
-    const float hi = __shfl_sync(0xffffffffu, acc[4 + i], lane >> 1);
+    const float lo = __shfl_sync(0xffffffffu, acc[i], 16 * half + (lane >> 1));
+    const float hi = __shfl_sync(0xffffffffu, acc[4 + i], 16 * half + (lane >> 1));
     m[i] = __fdiv_rn((lane & 1) ? hi : lo, count);
   }
   store_mean(means, flag, rows, row, lane, make_float4(m[0], m[1], m[2], m[3]));
@@ -137,60 +131,56 @@ __device__ __forceinline__ void store_half_mean(void* means, int flag, int64_t r
 constexpr int kWriteRows = 8;  // bf16 rows in flight per lane
 constexpr int kHeldRows = 16;  // 4-bit rows in flight per lane
 
-// One warp per (pair, block): rows below the old length come from the cache
-// (append; keys only, for the mean), the others are quantised and written.
-__global__ void __launch_bounds__(kKvThreads) kv4_write_kernel(Kv4WriteParams p) {
-  pdl_wait();
-  pdl_trigger_early();
-  const int lane = threadIdx.x & 31, half = lane >> 4, x = lane & 15;
-  const int64_t unit = (int64_t)blockIdx.x * kKvWarps + (threadIdx.x >> 5);
-  const int64_t pair = unit / p.span;
-  const int j = (int)(unit - pair * p.span);
-  if (pair >= (int64_t)p.B * p.Hkv) return;
+// Keys (kKeys) or values of two consecutive blocks of a pair, one each half of
+// the warp: rows below the old length come from the cache (append; keys only,
+// for the mean), the others are quantised and written.
+template <bool kKeys>
+__device__ __forceinline__ void write_blocks(const Kv4WriteParams& p, int64_t pair, int j, int lane) {
+  const int half = lane >> 4, x = lane & 15, g = x >> 2, c = x & 3;
   const int b = (int)(pair / p.Hkv), h = (int)(pair - (int64_t)b * p.Hkv);
   const int Lcap = p.dst.Lcap, bs = p.bs;
   const int len = __ldg(p.seq_lens + b);
   const int L0 = p.append ? len : 0;                                  // rows already held
   const int64_t L1w = p.append ? (int64_t)len + p.n_new : (int64_t)len;
-  if (len < 0 || L1w > Lcap) {
-    if (lane == 0 && j == 0) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
-    // the length stays as it was
-    if (p.append && h == 0 && j == 0 && lane == 0 && p.new_lens && p.new_lens != p.seq_lens) p.new_lens[b] = len;
-    return;
+  const bool bad = len < 0 || L1w > Lcap;
+  const int L1 = bad ? 0 : (int)L1w;
+  if (kKeys && h == 0 && j == 0 && lane == 0) {  // a sequence that does not fit keeps its length
+    if (p.append && p.new_lens != p.seq_lens) p.new_lens[b] = bad ? len : L1;
+    if (bad) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
   }
-  const int L1 = (int)L1w;
-  if (p.append && h == 0 && j == 0 && lane == 0 && p.new_lens && p.new_lens != p.seq_lens) p.new_lens[b] = L1;
-  const int i = L0 / bs + j;
-  const int t0 = i * bs, t1 = min(t0 + bs, L1);
-  if (t0 >= t1) return;
-  const int64_t row0 = kv_row(p.dst.pages, b, h, p.Hkv, Lcap, bs, t0);  // a block's rows are contiguous
-  const int tn = max(t0, L0);                                          // first new row
-  int64_t src0;                                                        // source row of token tn
-  if (p.append)
-    src0 = pair * p.n_new + (tn - L0);
-  else
-    src0 = kv_row(p.src_pages, b, h, p.Hkv, Lcap, bs, t0);
-  if (row0 < 0 || src0 < 0) {  // a page index outside its pool: the block is left as it was
-    if (lane == 0) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
-    return;
+  if (bad) return;
+  const int i = L0 / bs + j + half;
+  const int t0 = i * bs, tn = max(t0, L0);  // tn: the first new row
+  int t1 = j + half < p.span ? min(t0 + bs, L1) : t0;
+  int64_t row0 = 0, src0 = 0;               // a block's rows are contiguous, so are the new ones
+  if (t0 < t1) {
+    row0 = kv_row(p.dst.pages, b, h, p.Hkv, Lcap, bs, t0);
+    src0 = p.append ? pair * p.n_new + (tn - L0) : kv_row(p.src_pages, b, h, p.Hkv, Lcap, bs, t0);
+    if (row0 < 0 || src0 < 0) {  // a page index outside its pool: the block is left as it was
+      if (kKeys) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
+      t1 = t0;
+    }
   }
+  const int held = t0 < t1 ? tn - t0 : 0, fresh = t0 < t1 ? t1 - tn : 0;
+  const int most = max(fresh, __shfl_xor_sync(0xffffffffu, fresh, 16));
   float acc[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  const int g = x >> 2, c = x & 3;
-  if (p.means && half == 0) {  // held keys of the block, in token order
-    for (int t = t0; t < tn; t += kHeldRows) {
+  if (kKeys && p.means) {  // held keys of the block, in token order
+    const uint8_t* codes = p.dst.k + row0 * kCodeBytes + (4 * c + g) * 4;
+    const uint16_t* sc = p.dst.ks + row0 * kGroups + g;
+    for (int r = 0; r < held; r += kHeldRows) {
       uint32_t w[kHeldRows];
       uint16_t s[kHeldRows];
 #pragma unroll
       for (int u = 0; u < kHeldRows; ++u) {
-        const int64_t row = row0 + min(t + u, tn - 1) - t0;
-        w[u] = *reinterpret_cast<const uint32_t*>(p.dst.k + row * kCodeBytes + (4 * c + g) * 4);
-        s[u] = p.dst.ks[row * kGroups + g];
+        const int64_t row = min(r + u, held - 1);
+        w[u] = *reinterpret_cast<const uint32_t*>(codes + row * kCodeBytes);
+        s[u] = sc[row * kGroups];
       }
 #pragma unroll
       for (int u = 0; u < kHeldRows; ++u) {
-        if (t + u < tn) {
+        if (r + u < held) {
           float v[8];
           key_values(w[u], __uint_as_float((uint32_t)s[u] << 16), v);
 #pragma unroll
@@ -198,30 +188,62 @@ __global__ void __launch_bounds__(kKvThreads) kv4_write_kernel(Kv4WriteParams p)
         }
       }
     }
+    __syncwarp();
   }
-  __syncwarp();
-  const uint8_t* src = (half ? p.v_src : p.k_src) + src0 * (kHeadDim * 2) + x * 16;
-  for (int t = tn; t < t1; t += kWriteRows) {
+  const uint8_t* src = (kKeys ? p.k_src : p.v_src) + src0 * (kHeadDim * 2) + x * 16;
+  uint8_t* to = (kKeys ? p.dst.k : p.dst.v) + (row0 + held) * kCodeBytes + (kKeys ? (4 * c + g) * 4 : (8 * c + g) * 2);
+  uint16_t* to_s = (kKeys ? p.dst.ks : p.dst.vs) + (row0 + held) * kGroups + g;
+  for (int r = 0; r < most; r += kWriteRows) {
     uint4 w[kWriteRows];
 #pragma unroll
     for (int u = 0; u < kWriteRows; ++u)
-      w[u] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(min(t + u, t1 - 1) - tn) * (kHeadDim * 2)));
+      if (fresh > 0) w[u] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)min(r + u, fresh - 1) * (kHeadDim * 2)));
 #pragma unroll
     for (int u = 0; u < kWriteRows; ++u) {
-      if (t + u < t1) {  // warp-uniform
+      if (r + u < most) {  // warp-uniform
         float n[8];
         const uint32_t s = encode8(w[u], n);
-        write_row(p.dst, half, x, row0 + (t + u - t0), n, s);
-        const float sf = __uint_as_float(s << 16);
+        if (r + u < fresh) {
+          if (kKeys) {
+            *reinterpret_cast<uint32_t*>(to + (r + u) * kCodeBytes) =
+                __byte_perm(nibbles4(n[0], n[2], n[4], n[6]), nibbles4(n[1], n[3], n[5], n[7]), 0x5410);
+            const float sf = __uint_as_float(s << 16);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = fmaf(n[e], sf, acc[e]);  // the product is exact
+            for (int e = 0; e < 8; ++e) acc[e] = fmaf(n[e], sf, acc[e]);  // the product is exact
+          } else {
+            *reinterpret_cast<uint16_t*>(to + (r + u) * kCodeBytes) = (uint16_t)nibbles4(n[0], n[1], n[2], n[3]);
+            *reinterpret_cast<uint16_t*>(to + (r + u) * kCodeBytes + 8) = (uint16_t)nibbles4(n[4], n[5], n[6], n[7]);
+          }
+          if (c == 0) to_s[(r + u) * kGroups] = (uint16_t)s;
+        }
       }
     }
   }
-  if (p.means) {
-    const int64_t mrow = means_row_index(p.dst.pages, p.means_per_page, b, h, p.Hkv, p.nbcap, i);
-    if (mrow >= 0) store_half_mean(p.means, p.means_flag, p.mean_rows, mrow, lane, acc, (float)(t1 - t0));
+  if (kKeys && p.means) {
+    const int rows = held + fresh;
+#pragma unroll
+    for (int hb = 0; hb < 2; ++hb) {
+      const int n = __shfl_sync(0xffffffffu, rows, 16 * hb);
+      if (n > 0) {
+        const int64_t mrow = means_row_index(p.dst.pages, p.means_per_page, b, h, p.Hkv, p.nbcap, L0 / bs + j + hb);
+        store_half_mean(p.means, p.means_flag, p.mean_rows, mrow, lane, hb, acc, (float)n);
+      }
+    }
   }
+}
+
+__global__ void __launch_bounds__(kKvThreads) kv4_write_kernel(Kv4WriteParams p) {
+  pdl_wait();
+  pdl_trigger_early();
+  const int lane = threadIdx.x & 31, per = (p.span + 1) / 2;  // units of a pair, for keys and for values
+  const int64_t unit = (int64_t)blockIdx.x * kKvWarps + (threadIdx.x >> 5);
+  const int64_t of = unit >> 1, pair = of / per;
+  if (pair >= (int64_t)p.B * p.Hkv) return;
+  const int j = 2 * (int)(of - pair * per);
+  if (unit & 1)
+    write_blocks<false>(p, pair, j, lane);
+  else
+    write_blocks<true>(p, pair, j, lane);
 }
 
 // In-place advance of the lengths, after every CTA of the write has read them.
@@ -235,50 +257,66 @@ __global__ void __launch_bounds__(256) kv4_advance_kernel(int32_t* lens, int B, 
 }
 
 cudaError_t launch_kv4_write(const Kv4WriteParams& p, cudaStream_t s) {
-  const int64_t units = (int64_t)p.B * p.Hkv * p.span;
+  const int64_t units = 2 * (int64_t)p.B * p.Hkv * ((p.span + 1) / 2);
   cudaError_t e = launch_pdl(kv4_write_kernel, dim3((unsigned)((units + kKvWarps - 1) / kKvWarps)), dim3(kKvThreads), 0, s, p);
   if (e != cudaSuccess || !p.append || p.new_lens != p.seq_lens) return e;
   return launch_pdl(kv4_advance_kernel, dim3((p.B + 255) / 256), dim3(256), 0, s, p.new_lens, p.B, p.n_new, p.dst.Lcap);
 }
 
-constexpr int kLoadRows = 8;  // rows per warp
+constexpr int kLoadRows = 8;  // rows of a half warp
 
-// Rows back as bf16: one warp per kLoadRows consecutive output rows of a
-// pair, lower half keys, upper half values.
-__global__ void __launch_bounds__(kKvThreads) kv4_load_kernel(Kv4LoadParams p) {
-  pdl_wait();
-  pdl_trigger_early();
-  const int lane = threadIdx.x & 31, half = lane >> 4, x = lane & 15;
-  const int per = (p.n + kLoadRows - 1) / kLoadRows;
-  const int64_t unit = (int64_t)blockIdx.x * kKvWarps + (threadIdx.x >> 5);
-  const int64_t pair = unit / per;
-  const int r0 = (int)(unit - pair * per) * kLoadRows;
-  if (pair >= (int64_t)p.B * p.Hkv) return;
+__device__ __forceinline__ uint32_t hadd2_bf16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("{.reg .b32 one; mov.b32 one, 0x3F803F80; fma.rn.bf16x2 %0, %1, one, %2;}" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("{.reg .b32 zero; mov.b32 zero, 0x80008000; fma.rn.bf16x2 %0, %1, %2, zero;}" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Rows back as bf16: a warp has keys (kKeys) or values of 16 consecutive
+// output rows of a pair, a half 8 of them.  A nibble n becomes the bf16 number
+// 128 + n by one logic operation for two, less 136 the code, exact; its
+// product with the scale is rounded once.
+template <bool kKeys>
+__device__ __forceinline__ void load_rows(const Kv4LoadParams& p, int64_t pair, int unit, int lane) {
+  const int half = lane >> 4, x = lane & 15, g = x >> 2, c = x & 3;
   const int b = (int)(pair / p.Hkv), h = (int)(pair - (int64_t)b * p.Hkv);
+  const int r0 = unit * 2 * kLoadRows + half * kLoadRows;
   int L = __ldg(p.seq_lens + b);
   const int start = p.starts ? __ldg(p.starts + b) : 0;
   if (L < 0 || L > p.src.Lcap || start < 0) {
-    if (lane == 0 && r0 == 0) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
+    if (kKeys && unit == 0 && lane == 0) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
     L = 0;  // zeros
   }
-  const int g = x >> 2, c = x & 3;
-  uint32_t w[kLoadRows];
-  uint16_t s[kLoadRows];
+  const int rows = min(kLoadRows, p.n - r0);
+  const int live = (int)max((int64_t)0, min((int64_t)rows, (int64_t)L - start - r0));  // rows below the length
+  const int lbs = 31 - __clz(p.bs), t = start + r0;
+  const bool paged = p.src.pages.table != nullptr;
+  uint32_t w[kLoadRows], s[kLoadRows];
   bool bad = false;
+  int64_t row = live > 0 ? kv_row(p.src.pages, b, h, p.Hkv, p.src.Lcap, p.bs, t) : -1;
 #pragma unroll
   for (int u = 0; u < kLoadRows; ++u) {
     w[u] = 0x88888888u;
-    s[u] = 0;
-    const int64_t t = (int64_t)start + r0 + u;
-    if (r0 + u < p.n && t < L) {
-      const int64_t row = kv_row(p.src.pages, b, h, p.Hkv, p.src.Lcap, p.bs, (int)t);
+    s[u] = 0u;
+    if (u < live) {
+      if (u > 0) {
+        if (paged && ((t + u) & (p.bs - 1)) == 0)
+          row = kv_row(p.src.pages, b, h, p.Hkv, p.src.Lcap, p.bs, ((t + u) >> lbs) << lbs);
+        else if (row >= 0)
+          ++row;
+      }
       if (row >= 0) {
-        if (half == 0) {
+        if (kKeys) {
           w[u] = __ldg(reinterpret_cast<const uint32_t*>(p.src.k + row * kCodeBytes + (4 * c + g) * 4));
           s[u] = __ldg(p.src.ks + row * kGroups + g);
         } else {
-          const uint16_t* o = reinterpret_cast<const uint16_t*>(p.src.v + row * kCodeBytes);
-          w[u] = (uint32_t)__ldg(o + 8 * c + g) | ((uint32_t)__ldg(o + 8 * c + 4 + g) << 16);
+          const uint16_t* o = reinterpret_cast<const uint16_t*>(p.src.v + row * kCodeBytes) + 8 * c + g;
+          w[u] = (uint32_t)__ldg(o) | ((uint32_t)__ldg(o + 4) << 16);
           s[u] = __ldg(p.src.vs + row * kGroups + g);
         }
       } else {
@@ -287,31 +325,43 @@ __global__ void __launch_bounds__(kKvThreads) kv4_load_kernel(Kv4LoadParams p) {
     }
   }
   if (bad && x == 0) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
-  __nv_bfloat16* out = half ? p.v_out : p.k_out;
+  uint4* out = reinterpret_cast<uint4*>(kKeys ? p.k_out : p.v_out) + (pair * p.n + r0) * 16 + x;
 #pragma unroll
   for (int u = 0; u < kLoadRows; ++u) {
-    if (r0 + u < p.n) {
-      const float sf = __uint_as_float((uint32_t)s[u] << 16);
-      float v[8];
-      if (half == 0) {
-        key_values(w[u], sf, v);
-      } else {
+    if (u < rows) {
+      const uint32_t s2 = s[u] * 0x10001u;
+      uint32_t o[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = code_of(w[u], e) * sf;
+      for (int i = 0; i < 4; ++i) {
+        uint32_t y;
+        if (kKeys) {  // channels 2i, 2i + 1 in nibbles i, i + 4
+          y = w[u] >> (4 * i);
+        } else {  // in nibbles 2i, 2i + 1
+          const uint32_t v = w[u] >> (8 * i);
+          y = (v & 0xFu) | (v << 12);
+        }
+        o[i] = hmul2_bf16(hadd2_bf16((y & 0x000F000Fu) | 0x43004300u, 0xC308C308u), s2);
       }
-      // the product has up to 11 significant bits: one rounding to bf16
-      uint4 o;
-      o.x = pack_bf16x2(v[0], v[1]);
-      o.y = pack_bf16x2(v[2], v[3]);
-      o.z = pack_bf16x2(v[4], v[5]);
-      o.w = pack_bf16x2(v[6], v[7]);
-      reinterpret_cast<uint4*>(out)[(pair * p.n + r0 + u) * 16 + x] = o;
+      out[u * 16] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
 
+__global__ void __launch_bounds__(kKvThreads) kv4_load_kernel(Kv4LoadParams p) {
+  pdl_wait();
+  pdl_trigger_early();
+  const int lane = threadIdx.x & 31, per = (p.n + 2 * kLoadRows - 1) / (2 * kLoadRows);
+  const int64_t unit = (int64_t)blockIdx.x * kKvWarps + (threadIdx.x >> 5);
+  const int64_t of = unit >> 1, pair = of / per;
+  if (pair >= (int64_t)p.B * p.Hkv) return;
+  if (unit & 1)
+    load_rows<false>(p, pair, (int)(of - pair * per), lane);
+  else
+    load_rows<true>(p, pair, (int)(of - pair * per), lane);
+}
+
 cudaError_t launch_kv4_load(const Kv4LoadParams& p, cudaStream_t s) {
-  const int64_t units = (int64_t)p.B * p.Hkv * ((p.n + kLoadRows - 1) / kLoadRows);
+  const int64_t units = 2 * (int64_t)p.B * p.Hkv * ((p.n + 2 * kLoadRows - 1) / (2 * kLoadRows));
   return launch_pdl(kv4_load_kernel, dim3((unsigned)((units + kKvWarps - 1) / kKvWarps)), dim3(kKvThreads), 0, s, p);
 }
 
@@ -409,7 +459,7 @@ __global__ void __launch_bounds__(kKvThreads) evict_move_kernel(EvictParams p) {
   if (bad) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);  // the row is left as it was
   if (p.means) {
     const int64_t mrow = means_row_index(p.dst.pages, p.means_per_page, b, h, p.Hkv, p.nbcap_dst, i);
-    if (mrow >= 0) store_half_mean(p.means, p.means_flag, p.mean_rows, mrow, lane, acc, (float)(t1 - t0));
+    if (mrow >= 0) store_half_mean(p.means, p.means_flag, p.mean_rows, mrow, lane, 0, acc, (float)(t1 - t0));
   }
 }
 
