@@ -133,7 +133,7 @@ cudaError_t ensure_smem_limit(const void* kernel, int slot, size_t bytes) {
   // device) never exceeds the limit in force.
   // slots in use: 0, 2, 3, then 8, 9, 10, then 12, 13, 14 block top-k (256,
   // 512, 1024 threads; plain, refining, refining per page), 1 attention, 4
-  // means update, 5 token top-k, 6 token logits, 7 eviction select, 16..19
+  // means update, 5 token top-k, 6 token logits, 7 and 11 eviction select, 16..19
   // attention over a cache of either format
   static std::atomic<size_t> done[kSmemSlots][kMaxDevices];
   static std::mutex mu;

@@ -366,105 +366,141 @@ cudaError_t launch_kv4_load(const Kv4LoadParams& p, cudaStream_t s) {
 }
 
 // ------------------------------------------------------------- eviction: move
-// One warp per (pair, destination block): the kept tokens' rows, scales and
-// weights move to their new places (ascending, so blocks keep the time order)
-// and the block's mean is taken on the way.  Destination weights behind the
-// kept tokens become zero, so tokens appended later start at nothing.  Rows
-// are gathered, 8 in flight per lane.
-template <bool kInt4>
-__global__ void __launch_bounds__(kKvThreads) evict_move_kernel(EvictParams p) {
-  pdl_wait();
-  pdl_trigger_early();
-  const int lane = threadIdx.x & 31, half = lane >> 4, x = lane & 15;
-  const int64_t unit = (int64_t)blockIdx.x * kKvWarps + (threadIdx.x >> 5);
-  const int64_t pair = unit / p.nbcap_dst;
-  const int i = (int)(unit - pair * p.nbcap_dst);
-  if (pair >= (int64_t)p.B * p.Hkv) return;
+// The kept tokens' rows, scales and weights move to their new places
+// (ascending, so blocks keep the time order) and the blocks' means are taken
+// on the way.  A warp has keys or values of two consecutive destination
+// blocks, one each half; rows are gathered, 8 in flight per lane (16 of
+// 4 bits cost more in registers than they hid).  Destination
+// weights behind the kept tokens become zero, so tokens appended later start
+// at nothing.
+template <bool kInt4, bool kKeys>
+__device__ __forceinline__ void move_blocks(const EvictParams& p, int64_t pair, int i0, int lane) {
+  constexpr uint32_t kNone = 0xFFFFFFFFu;
+  constexpr int kFly = 8;  // rows in flight per lane
+  const int half = lane >> 4, x = lane & 15, g = x >> 2, c = x & 3;
   const int b = (int)(pair / p.Hkv), h = (int)(pair - (int64_t)b * p.Hkv);
-  const int bs = p.bs;
+  const int bs = p.bs, lbs = 31 - __clz(bs);
   const int m = __ldg(p.dst_lens + b);  // written by the select kernel: min(L, n_keep), 0 for a bad length
-  const int t0 = i * bs, t1 = min(t0 + bs, m);
-  const int32_t* sel = p.sel + pair * p.n_keep;
-  if (p.dst_acc) {
-    const int end = min(t0 + bs, p.dst.Lcap);
-    for (int t = t0 + lane; t < end; t += 32)
-      p.dst_acc[pair * p.dst.Lcap + t] = t < t1 ? __ldg(p.acc + pair * p.src.Lcap + __ldg(sel + t)) : 0.f;
+  const int i = i0 + half, t0 = i << lbs;
+  int n = max(0, min(bs, m - t0));  // this half's rows
+  const int32_t* sel = p.sel + pair * p.n_keep + t0;
+  if (kKeys && p.dst_acc) {
+    const int end = min(bs, p.dst.Lcap - t0);
+    for (int r = x; r < end; r += 16)
+      p.dst_acc[pair * p.dst.Lcap + t0 + r] = r < n ? __ldg(p.acc + pair * p.src.Lcap + __ldg(sel + r)) : 0.f;
   }
-  if (t0 >= t1) return;
-  const int64_t to0 = kv_row(p.dst.pages, b, h, p.Hkv, p.dst.Lcap, bs, t0);
-  if (to0 < 0) {
-    if (lane == 0) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
-    return;
+  int64_t to0 = 0;
+  if (n > 0) {
+    to0 = kv_row(p.dst.pages, b, h, p.Hkv, p.dst.Lcap, bs, t0);
+    if (to0 < 0) {
+      if (kKeys) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
+      n = 0;
+    }
   }
-  const int g = x >> 2, c = x & 3;
+  const int most = max(n, __shfl_xor_sync(0xffffffffu, n, 16));
+  // a lane's bytes of a row: 16 of a bf16 row; of a 4-bit row the key word of
+  // its 8 channels or the x-th value word, and its group's scale
+  const int at = kInt4 ? (kKeys ? (4 * c + g) * 4 : x * 4) : x * 16;
+  constexpr int kRow = kInt4 ? kCodeBytes : kHeadDim * 2;
+  const uint8_t* src = (kKeys ? p.src.k : p.src.v) + at;
+  uint8_t* dst = (kKeys ? p.dst.k : p.dst.v) + to0 * kRow + at;
+  const uint16_t* src_s = (kKeys ? p.src.ks : p.src.vs) + g;
+  uint16_t* dst_s = (kKeys ? p.dst.ks : p.dst.vs) + to0 * kGroups + g;
   float acc[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
   bool bad = false;
-  for (int tb = t0; tb < t1; tb += 32) {
-    int64_t my = -1;  // lane's source row
-    if (tb + lane < t1) {
-      my = kv_row(p.src.pages, b, h, p.Hkv, p.src.Lcap, bs, __ldg(sel + tb + lane));
-      bad |= my < 0;
+  for (int r0 = 0; r0 < most; r0 += 16) {
+    uint32_t my = kNone;  // lane's source row (a cache of 2^32 rows is larger than the memory)
+    if (r0 + x < n) {
+      const int t = __ldg(sel + r0 + x);
+      if (p.src.pages.table) {
+        const int page = __ldg(p.src.pages.table + (int64_t)b * p.src.pages.max_blocks + (t >> lbs));
+        if (page >= 0 && page < p.src.pages.num_pages)
+          my = ((uint32_t)(page * p.Hkv + h) << lbs) + (t & (bs - 1));
+        else
+          bad = true;
+      } else {
+        my = (uint32_t)pair * (uint32_t)p.src.Lcap + (uint32_t)t;
+      }
     }
-    const int n = min(32, t1 - tb);
-    for (int u0 = 0; u0 < n; u0 += 8) {
-      uint4 w[8];
-      uint16_t s[8];
-      int64_t from[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int src_lane = (u0 + u) & 31;
-        from[u] = (int64_t)(((uint64_t)(uint32_t)__shfl_sync(0xffffffffu, (int)(my >> 32), src_lane) << 32) |
-                            (uint32_t)__shfl_sync(0xffffffffu, (int)(uint32_t)my, src_lane));
-        w[u] = make_uint4(0u, 0u, 0u, 0u);
-        s[u] = 0;
-        if (u0 + u < n && from[u] >= 0) {
-          if constexpr (kInt4) {
-            const uint8_t* codes = half ? p.src.v : p.src.k;
-            w[u].x = __ldg(reinterpret_cast<const uint32_t*>(codes + from[u] * kCodeBytes + (4 * c + g) * 4));
-            s[u] = __ldg((half ? p.src.vs : p.src.ks) + from[u] * kGroups + g);
-          } else {
-            w[u] = __ldg(reinterpret_cast<const uint4*>((half ? p.src.v : p.src.k) + from[u] * (kHeadDim * 2) + x * 16));
-          }
+    for (int u0 = 0; u0 < 16; u0 += kFly) {
+      if (r0 + u0 >= most) break;  // warp-uniform
+      uint4 w[kFly];
+      uint32_t s[kFly], from[kFly];
+#pragma unroll
+      for (int u = 0; u < kFly; ++u) {
+        from[u] = __shfl_sync(0xffffffffu, my, 16 * half + u0 + u);
+        const uint64_t row = from[u] != kNone ? from[u] : 0u;  // every load goes out, row 0 in place of none
+        if constexpr (kInt4) {
+          w[u].x = __ldg(reinterpret_cast<const uint32_t*>(src + row * kRow));
+          s[u] = __ldg(src_s + row * kGroups);
+        } else {
+          w[u] = __ldg(reinterpret_cast<const uint4*>(src + row * kRow));
         }
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        if (u0 + u < n && from[u] >= 0) {
-          const int64_t to = to0 + (tb - t0) + u0 + u;
-          float v[8];
+      for (int u = 0; u < kFly; ++u) {
+        if (from[u] != kNone) {
+          const int r = r0 + u0 + u;
           if constexpr (kInt4) {
-            uint8_t* codes = half ? p.dst.v : p.dst.k;
-            *reinterpret_cast<uint32_t*>(codes + to * kCodeBytes + (4 * c + g) * 4) = w[u].x;
-            if (c == 0) (half ? p.dst.vs : p.dst.ks)[to * kGroups + g] = s[u];
-            key_values(w[u].x, __uint_as_float((uint32_t)s[u] << 16), v);
+            *reinterpret_cast<uint32_t*>(dst + r * kRow) = w[u].x;
+            if (c == 0) dst_s[r * kGroups] = (uint16_t)s[u];
           } else {
-            *reinterpret_cast<uint4*>((half ? p.dst.v : p.dst.k) + to * (kHeadDim * 2) + x * 16) = w[u];
-            v[0] = bf16_lo(w[u].x);
-            v[1] = bf16_hi(w[u].x);
-            v[2] = bf16_lo(w[u].y);
-            v[3] = bf16_hi(w[u].y);
-            v[4] = bf16_lo(w[u].z);
-            v[5] = bf16_hi(w[u].z);
-            v[6] = bf16_lo(w[u].w);
-            v[7] = bf16_hi(w[u].w);
+            *reinterpret_cast<uint4*>(dst + r * kRow) = w[u];
           }
+          if constexpr (kKeys) {
+            if constexpr (kInt4) {
+              float v[8];
+              key_values(w[u].x, __uint_as_float(s[u] << 16), v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] += v[e];
+              for (int e = 0; e < 8; ++e) acc[e] += v[e];
+            } else {
+              acc[0] += bf16_lo(w[u].x);
+              acc[1] += bf16_hi(w[u].x);
+              acc[2] += bf16_lo(w[u].y);
+              acc[3] += bf16_hi(w[u].y);
+              acc[4] += bf16_lo(w[u].z);
+              acc[5] += bf16_hi(w[u].z);
+              acc[6] += bf16_lo(w[u].w);
+              acc[7] += bf16_hi(w[u].w);
+            }
+          }
         }
       }
     }
   }
-  if (bad) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);  // the row is left as it was
-  if (p.means) {
-    const int64_t mrow = means_row_index(p.dst.pages, p.means_per_page, b, h, p.Hkv, p.nbcap_dst, i);
-    if (mrow >= 0) store_half_mean(p.means, p.means_flag, p.mean_rows, mrow, lane, 0, acc, (float)(t1 - t0));
+  if (kKeys && bad) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);  // the row is left as it was
+  if (kKeys && p.means) {
+#pragma unroll
+    for (int hb = 0; hb < 2; ++hb) {
+      const int rows = __shfl_sync(0xffffffffu, n, 16 * hb);
+      if (rows > 0) {
+        const int64_t mrow = means_row_index(p.dst.pages, p.means_per_page, b, h, p.Hkv, p.nbcap_dst, i0 + hb);
+        store_half_mean(p.means, p.means_flag, p.mean_rows, mrow, lane, hb, acc, (float)rows);
+      }
+    }
   }
 }
 
+template <bool kInt4>
+__global__ void __launch_bounds__(kKvThreads) evict_move_kernel(EvictParams p) {
+  pdl_wait();
+  pdl_trigger_early();
+  const int lane = threadIdx.x & 31, per = (p.nbcap_dst + 1) / 2;
+  const int64_t unit = (int64_t)blockIdx.x * kKvWarps + (threadIdx.x >> 5);
+  const int64_t of = unit >> 1, pair = of / per;
+  if (pair >= (int64_t)p.B * p.Hkv) return;
+  const int i0 = 2 * (int)(of - pair * per);
+  if (unit & 1)
+    move_blocks<kInt4, false>(p, pair, i0, lane);
+  else
+    move_blocks<kInt4, true>(p, pair, i0, lane);
+}
+
 cudaError_t launch_evict_move(const EvictParams& p, cudaStream_t s) {
-  const int64_t units = (int64_t)p.B * p.Hkv * p.nbcap_dst;
+  const int64_t units = 2 * (int64_t)p.B * p.Hkv * ((p.nbcap_dst + 1) / 2);
   const dim3 grid((unsigned)((units + kKvWarps - 1) / kKvWarps));
   return p.src.int4 ? launch_pdl(evict_move_kernel<true>, grid, dim3(kKvThreads), 0, s, p)
                     : launch_pdl(evict_move_kernel<false>, grid, dim3(kKvThreads), 0, s, p);

@@ -522,6 +522,11 @@ __device__ __forceinline__ int sub_bin(float x, int bin) {
   return min(max((int)f, 0), 255);
 }
 
+// KeyOf maps a score's bits to its key.
+struct ScoreKey {
+  static __device__ __forceinline__ uint32_t of(uint32_t u) { return key_of_bits(u); }
+};
+
 // The equal-width-bin search fused with the emit, for rows whose emit ranges
 // are one round per warp (nb <= 1024 warps): the bin histogram (any order),
 // then one pass in the emit's ownership (lane l of warp w: the 32 keys from
@@ -730,11 +735,6 @@ __device__ __forceinline__ void select_from_keys(const uint32_t* keys, uint8_t* 
 // smallest and largest candidate key, and zeroes both histograms.  With both
 // rows 16-byte aligned, whole groups of 4 scores move as 16-byte loads and
 // stores, 8 per thread in flight; the rest one score at a time.
-// KeyOf maps a score's bits to its key.
-struct ScoreKey {
-  static __device__ __forceinline__ uint32_t of(uint32_t u) { return key_of_bits(u); }
-};
-
 template <int NT, typename KeyOf = ScoreKey>
 __device__ __forceinline__ void load_keys(const uint32_t* sc, uint32_t* keys, int nb, const Cands& cd, TopkSmem<NT>& sm,
                                           uint32_t& kmin, uint32_t& kmax) {
@@ -1996,15 +1996,16 @@ struct WeightKey {
   }
 };
 
-// One 1024-thread CTA per (sequence, KV head): the first n_sink and the last
+// One CTA of NT threads per (sequence, KV head): the first n_sink and the last
 // n_recent tokens are forced, the rest of the n_keep slots go to the largest
 // weights (ties to the lower index), ascending; every token when the budget
 // covers the length.  The threshold search is the token top-k's, over the
 // candidate range [n_sink, L - n_recent).  The first head's CTA writes the
 // sequence's new length.
-__global__ void __launch_bounds__(kTokTopkThreads, 1) evict_select_kernel(EvictParams p) {
+template <int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(EvictParams p) {
   extern __shared__ uint32_t skey[];  // as token_topk_kernel's
-  __shared__ TopkSmem<kTokTopkThreads> sm;
+  __shared__ TopkSmem<NT> sm;
   const int tid = threadIdx.x;
   pdl_wait();
   pdl_trigger_early();
@@ -2020,26 +2021,34 @@ __global__ void __launch_bounds__(kTokTopkThreads, 1) evict_select_kernel(EvictP
   }
   if (h == 0 && tid == 0) p.dst_lens[b] = min(L, k);
   if (L <= k) {
-    for (int i = tid; i < k; i += kTokTopkThreads) sel[i] = i < L ? i : -1;
+    for (int i = tid; i < k; i += NT) sel[i] = i < L ? i : -1;
     return;
   }
   const uint32_t* row = reinterpret_cast<const uint32_t*>(p.acc + pair * Lcap);
   const Cands cd{p.n_sink, L - p.n_recent - 1, k - p.n_sink - p.n_recent};
-  if (L <= 4 * kTokTopkThreads)
-    topk_regs<kTokTopkThreads, 4, WeightKey>(row, L, cd, k, sel, skey, sm, p.dev_status);
-  else if (L <= 8 * kTokTopkThreads)
-    topk_regs<kTokTopkThreads, 8, WeightKey>(row, L, cd, k, sel, skey, sm, p.dev_status);
+  if (L <= 4 * NT)
+    topk_regs<NT, 4, WeightKey>(row, L, cd, k, sel, skey, sm, p.dev_status);
+  else if (L <= 8 * NT)
+    topk_regs<NT, 8, WeightKey>(row, L, cd, k, sel, skey, sm, p.dev_status);
   else
-    topk_memory<kTokTopkThreads, WeightKey>(row, L, cd, k, sel, skey, min(Lcap, kTokKeyCap),
+    topk_memory<NT, WeightKey>(row, L, cd, k, sel, skey, min(Lcap, kTokKeyCap),
                                             p.key_scratch + pair * Lcap, sm, p.dev_status);
 }
 
-cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s) {
+template <int NT>
+static cudaError_t launch_evict_select_as(const EvictParams& p, cudaStream_t s) {
   const size_t cap = (size_t)(p.src.Lcap < kTokKeyCap ? p.src.Lcap : kTokKeyCap);
   const size_t smem = cap * sizeof(uint32_t) + ((cap + 3) & ~size_t(3));  // keys, then their bins
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(evict_select_kernel), 7, smem);
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(evict_select_kernel<NT>), NT == 512 ? 11 : 7, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(evict_select_kernel, dim3(p.B * p.Hkv), dim3(kTokTopkThreads), smem, s, p);
+  return launch_pdl(evict_select_kernel<NT>, dim3(p.B * p.Hkv), dim3(NT), smem, s, p);
+}
+
+// 1024 threads, or two CTAs of 512 on an SM where there are more pairs than
+// SMs and the fused search still covers a row (1024 keys a warp).
+cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s) {
+  const bool two = (int64_t)p.B * p.Hkv > device_sm_count() && p.src.Lcap <= 512 * 32;
+  return two ? launch_evict_select_as<512>(p, s) : launch_evict_select_as<1024>(p, s);
 }
 
 // Threads per top-k CTA: enough for 4 keys per thread (up to 4096 blocks),
