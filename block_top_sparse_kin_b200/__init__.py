@@ -162,6 +162,10 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None, nullable=False, count
         if nullable:
             return None
         raise ValueError(f"{name} is required")
+    if (t.is_cuda and t.get_device() == _current_device() and t.is_contiguous()
+            and (dtype is None or t.dtype is dtype or (dtype.__class__ is tuple and t.dtype in dtype))
+            and (count is None or t.numel() >= count)):
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.get_device() != _current_device():
@@ -171,9 +175,7 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None, nullable=False, count
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype is not dtype and (not isinstance(dtype, tuple) or t.dtype not in dtype):
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if count is not None and t.numel() < count:
-        raise ValueError(f"{name} holds {t.numel()} elements; the dims need {count}")
-    return t.data_ptr()
+    raise ValueError(f"{name} holds {t.numel()} elements; the dims need {count}")
 
 
 class _Counts:
@@ -515,36 +517,60 @@ def kin_block_topk_select_paged(dims, q, page_means, block_table, seq_lens, k_bl
 class KvCache:
     """A KV cache as the kin_kv_* calls take it: bf16 rows (no scales), or
     4-bit codes (uint8) with their bf16 scales; contiguous, or a page pool
-    with its block_table.  Holds the tensors it is made of."""
+    with its block_table.  Holds the tensors it is made of; their types,
+    device and layout are checked at the first call that takes it, their
+    places (they must stay where they are) and sizes at every one."""
 
-    __slots__ = ("k", "v", "k_scales", "v_scales", "block_table")
+    __slots__ = ("_k", "_v", "_k_scales", "_v_scales", "_block_table", "_c", "_at", "_device")
 
     def __init__(self, k, v, k_scales=None, v_scales=None, block_table=None):
         if (k_scales is None) != (v_scales is None):
             raise ValueError("a 4-bit cache has k_scales and v_scales")
-        self.k, self.v, self.k_scales, self.v_scales, self.block_table = k, v, k_scales, v_scales, block_table
+        self._k, self._v, self._k_scales, self._v_scales, self._block_table = k, v, k_scales, v_scales, block_table
+        self._c = None
+
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    k_scales = property(lambda self: self._k_scales)
+    v_scales = property(lambda self: self._v_scales)
+    block_table = property(lambda self: self._block_table)
 
     @property
     def int4(self) -> bool:
-        return self.k_scales is not None
+        return self._k_scales is not None
+
+    def _tensors(self):
+        return [t for t in (self._k, self._v, self._k_scales, self._v_scales, self._block_table) if t is not None]
 
     def _struct(self, c: "_Counts", name: str):
-        """The C descriptor, after the checks every call makes of its tensors."""
-        pages, table, elements = 0, None, c.cache
-        if self.block_table is not None:
-            pages = int(self.k.shape[0])
-            table = _dev(self.block_table, f"{name}.block_table", torch.int32, count=c.table)
-            elements = c.times(pages, c.page)
-        if self.k_scales is None:
-            return kin_kv(KIN_KV_BF16, pages, table, _dev(self.k, f"{name}.k", _BF16, count=elements),
-                          _dev(self.v, f"{name}.v", _BF16, count=elements), None, None), pages
-        codes = scales = None
-        if elements is not None:
-            codes, scales = elements >> 1, elements >> 5
-        return kin_kv(KIN_KV_INT4, pages, table, _dev(self.k, f"{name}.k", torch.uint8, count=codes),
-                      _dev(self.v, f"{name}.v", torch.uint8, count=codes),
-                      _dev(self.k_scales, f"{name}.k_scales", _BF16, count=scales),
-                      _dev(self.v_scales, f"{name}.v_scales", _BF16, count=scales)), pages
+        """The C descriptor and the pool's pages, after the checks every call makes of its tensors."""
+        if self._c is None:
+            pages = 0 if self._block_table is None else int(self._k.shape[0])
+            rows = torch.uint8 if self.int4 else _BF16
+            table = None if self._block_table is None else _dev(self._block_table, f"{name}.block_table", torch.int32)
+            scales = (_dev(self._k_scales, f"{name}.k_scales", _BF16), _dev(self._v_scales, f"{name}.v_scales", _BF16)) \
+                if self.int4 else (None, None)
+            self._c = kin_kv(KIN_KV_INT4 if self.int4 else KIN_KV_BF16, pages, table, _dev(self._k, f"{name}.k", rows),
+                             _dev(self._v, f"{name}.v", rows), *scales)
+            self._at = [t.data_ptr() for t in self._tensors()]
+            self._device = _current_device()
+        if self._device != _current_device():
+            raise ValueError(f"{name} is on cuda:{self._device}; the calls run on the current device")
+        if [t.data_ptr() for t in self._tensors()] != self._at:
+            raise ValueError(f"{name}: a tensor of the cache has moved since its first call")
+        if c.ok:
+            elements = c.cache if self._block_table is None else self._c.num_pages * c.page
+            if self._k_scales is None:
+                sizes = ((self._k, elements, "k"), (self._v, elements, "v"))
+            else:
+                sizes = ((self._k, elements >> 1, "k"), (self._v, elements >> 1, "v"),
+                         (self._k_scales, elements >> 5, "k_scales"), (self._v_scales, elements >> 5, "v_scales"))
+            for t, need, of in sizes:
+                if t.numel() < need:
+                    raise ValueError(f"{name}.{of} holds {t.numel()} elements; the dims need {need}")
+            if self._block_table is not None and self._block_table.numel() < c.table:
+                raise ValueError(f"{name}.block_table holds {self._block_table.numel()} elements; the dims need {c.table}")
+        return self._c, self._c.num_pages
 
 
 def alloc_kv4(dims: kin_dims, num_pages: Optional[int] = None, block_table=None, device="cuda") -> KvCache:

@@ -717,7 +717,7 @@ struct KvWs {
 
 // The select's regions first (its counters' place is this call's too), so
 // that one buffer serves both.
-KvWs kv_ws_layout(const kin_dims& d, int k_blocks, bool acc) {
+KvWs kv_ws_layout(const kin_dims& d, int k_blocks, const KvSplit& split, bool acc) {
   KvWs w;
   const size_t pairs = (size_t)pairs_of(d), g = (size_t)(d.num_q_heads / d.num_kv_heads);
   const int k = kv_slots(d, k_blocks);
@@ -725,7 +725,7 @@ KvWs kv_ws_layout(const kin_dims& d, int k_blocks, bool acc) {
   w.counters = 0;
   off = k_blocks >= 2 ? ws_layout(d, k_blocks).total : align_up(pairs * sizeof(uint32_t));
   w.partials = off;
-  off = align_up(off + pairs * (size_t)kv_max_chunks(k, kv_split(d, k, k_blocks == 0)) * g * kPartStride * sizeof(float));
+  off = align_up(off + pairs * (size_t)kv_max_chunks(k, split) * g * kPartStride * sizeof(float));
   w.z = off;
   if (acc) off = align_up(off + pairs * (size_t)k * d.block_size * g * sizeof(float));
   w.lse2 = off;
@@ -824,7 +824,8 @@ KIN_EXPORT kin_status kin_kv4_load(const kin_dims* dims, const kin_kv* kv, const
 
 KIN_EXPORT size_t kin_kv_attn_workspace_bytes(const kin_dims* dims, int32_t k_blocks, int32_t with_acc) {
   if (check_dims(dims) != KIN_OK || k_blocks < 0 || k_blocks == 1) return 0;
-  return kv_ws_layout(*dims, k_blocks, with_acc != 0).total;
+  const KvSplit split = kv_split(*dims, kv_slots(*dims, k_blocks), k_blocks == 0);
+  return kv_ws_layout(*dims, k_blocks, split, with_acc != 0).total;
 }
 
 KIN_EXPORT kin_status kin_kv_decode_attn(const kin_dims* dims, const void* q, const kin_kv* kv, const int32_t* seq_lens,
@@ -841,7 +842,8 @@ KIN_EXPORT kin_status kin_kv_decode_attn(const kin_dims* dims, const void* q, co
   if ((st = kv_view(*dims, kv, &p.kv)) != KIN_OK) return st;
   if (!q || !seq_lens || !out || !aligned16(q) || !aligned16(out)) return KIN_ERR_INVALID_ARG;
   if (!(softmax_scale == softmax_scale) || std::isinf(softmax_scale)) return KIN_ERR_INVALID_ARG;
-  const KvWs w = kv_ws_layout(*dims, k_blocks, acc != nullptr);
+  const KvSplit split = kv_split(*dims, kv_slots(*dims, k_blocks), k_blocks == 0);
+  const KvWs w = kv_ws_layout(*dims, k_blocks, split, acc != nullptr);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0 || ws_bytes < w.total)
     return KIN_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -864,7 +866,6 @@ KIN_EXPORT kin_status kin_kv_decode_attn(const kin_dims* dims, const void* q, co
   p.bs = dims->block_size;
   p.k_row = k_blocks;
   p.k = kv_slots(*dims, k_blocks);
-  const KvSplit split = kv_split(*dims, p.k, k_blocks == 0);
   p.per = split.per;
   p.stride = split.stride;
   if ((int64_t)pairs_of(*dims) * p.stride >= (int64_t)1 << 31) return KIN_ERR_CAPACITY;
