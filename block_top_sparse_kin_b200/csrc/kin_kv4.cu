@@ -197,7 +197,7 @@ __device__ __forceinline__ void write_blocks(const Kv4WriteParams& p, int64_t pa
     uint4 w[kWriteRows];
 #pragma unroll
     for (int u = 0; u < kWriteRows; ++u)
-      if (fresh > 0) w[u] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)min(r + u, fresh - 1) * (kHeadDim * 2)));
+      w[u] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)max(min(r + u, fresh - 1), 0) * (kHeadDim * 2)));
 #pragma unroll
     for (int u = 0; u < kWriteRows; ++u) {
       if (r + u < most) {  // warp-uniform
@@ -294,37 +294,39 @@ __device__ __forceinline__ void load_rows(const Kv4LoadParams& p, int64_t pair, 
   }
   const int rows = min(kLoadRows, p.n - r0);
   const int live = (int)max((int64_t)0, min((int64_t)rows, (int64_t)L - start - r0));  // rows below the length
-  const int lbs = 31 - __clz(p.bs), t = start + r0;
-  const bool paged = p.src.pages.table != nullptr;
+  // the rows: up to the block's end from one place, then from another (a block
+  // holds 16 at least); every load goes out, at row 0 where there is none
+  const int lbs = 31 - __clz(p.bs), t = live > 0 ? start + r0 : 0, cross = p.bs - (t & (p.bs - 1));
+  int64_t first = 0, second = 0;
+  bool good1 = false, good2 = false;
+  if (live > 0) {
+    first = kv_row(p.src.pages, b, h, p.Hkv, p.src.Lcap, p.bs, t);
+    good1 = good2 = first >= 0;
+    second = first;
+    if (p.src.pages.table && cross < live) {
+      second = kv_row(p.src.pages, b, h, p.Hkv, p.src.Lcap, p.bs, ((t >> lbs) + 1) << lbs) - cross;
+      good2 = second + cross >= 0;
+    }
+    if (!(good1 && good2) && x == 0) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
+  }
   uint32_t w[kLoadRows], s[kLoadRows];
-  bool bad = false;
-  int64_t row = live > 0 ? kv_row(p.src.pages, b, h, p.Hkv, p.src.Lcap, p.bs, t) : -1;
 #pragma unroll
   for (int u = 0; u < kLoadRows; ++u) {
-    w[u] = 0x88888888u;
-    s[u] = 0u;
-    if (u < live) {
-      if (u > 0) {
-        if (paged && ((t + u) & (p.bs - 1)) == 0)
-          row = kv_row(p.src.pages, b, h, p.Hkv, p.src.Lcap, p.bs, ((t + u) >> lbs) << lbs);
-        else if (row >= 0)
-          ++row;
-      }
-      if (row >= 0) {
-        if (kKeys) {
-          w[u] = __ldg(reinterpret_cast<const uint32_t*>(p.src.k + row * kCodeBytes + (4 * c + g) * 4));
-          s[u] = __ldg(p.src.ks + row * kGroups + g);
-        } else {
-          const uint16_t* o = reinterpret_cast<const uint16_t*>(p.src.v + row * kCodeBytes) + 8 * c + g;
-          w[u] = (uint32_t)__ldg(o) | ((uint32_t)__ldg(o + 4) << 16);
-          s[u] = __ldg(p.src.vs + row * kGroups + g);
-        }
-      } else {
-        bad = true;
-      }
+    const bool there = u < live && (u < cross ? good1 : good2);
+    const int64_t row = there ? (u < cross ? first : second) + u : 0;
+    if (kKeys) {
+      w[u] = __ldg(reinterpret_cast<const uint32_t*>(p.src.k + row * kCodeBytes + (4 * c + g) * 4));
+      s[u] = __ldg(p.src.ks + row * kGroups + g);
+    } else {
+      const uint16_t* o = reinterpret_cast<const uint16_t*>(p.src.v + row * kCodeBytes) + 8 * c + g;
+      w[u] = (uint32_t)__ldg(o) | ((uint32_t)__ldg(o + 4) << 16);
+      s[u] = __ldg(p.src.vs + row * kGroups + g);
+    }
+    if (!there) {  // a zero
+      w[u] = 0x88888888u;
+      s[u] = 0u;
     }
   }
-  if (bad && x == 0) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
   uint4* out = reinterpret_cast<uint4*>(kKeys ? p.k_out : p.v_out) + (pair * p.n + r0) * 16 + x;
 #pragma unroll
   for (int u = 0; u < kLoadRows; ++u) {
