@@ -45,6 +45,31 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+constexpr float kGrid = 0x1.8p11f, kWhole = 0x1.8p23f - 0x1.8p11f;  // see encode8
+
+struct Codes8 {
+  float c[8];
+};
+
+// encode8's codes where the scale is below 2^-100, zero or NaN: zero and NaN
+// give codes of 0.  Otherwise x and s are first scaled by 2^100 (exact), since
+// 1 / s overflows below 2^-126; a subnormal scale may be rounded by half, so
+// the quotient is cut at 7.  Its own function: inlined, it would double the
+// code of the paths that run.
+__device__ __noinline__ Codes8 encode8_tiny(uint4 w, float sf) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  const bool some = sf > 0.f;
+  const float inv = some ? __frcp_rn(sf * 0x1p100f) : 0.f;
+  Codes8 r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = some ? ((i & 1) ? bf16_hi(v[i >> 1]) : bf16_lo(v[i >> 1])) * 0x1p100f : 0.f;
+    const float y = fminf(fmaxf(x * inv, -7.f), 7.f);
+    r.c[i] = __fsub_rn(__fadd_rn(__fadd_rn(y, kGrid), kWhole), 12582912.f);
+  }
+  return r;
+}
+
 // 8 channels of a group in 4 bits: w = the bf16 pairs of this lane.  Returns
 // the scale's bits (the same in the group's 4 lanes) and the codes c[i] as
 // numbers.
@@ -70,7 +95,6 @@ __device__ __forceinline__ uint32_t encode8(const uint4& w, float (&c)[8]) {
   const uint32_t s = m < 0x7F80u ? (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(m << 16) * 0x1.24924ap-3f))
                                  : 0x7FC0u;
   const float sf = __uint_as_float(s << 16);
-  constexpr float kGrid = 0x1.8p11f, kWhole = 0x1.8p23f - 0x1.8p11f;
   if (sf >= 0x1p-100f) {
     const float inv = rcp_approx(sf);  // to 2^-23
 #pragma unroll
@@ -79,17 +103,9 @@ __device__ __forceinline__ uint32_t encode8(const uint4& w, float (&c)[8]) {
       c[i] = __fsub_rn(__fadd_rn(__fmaf_rn(x, inv, kGrid), kWhole), 12582912.f);
     }
   } else {
-    // a scale of zero, or NaN: every code is 0.  A tiny one: x and s are first
-    // scaled by 2^100 (exact), since 1 / s overflows below 2^-126; a subnormal
-    // scale may be rounded by half, so the quotient is cut at 7.
-    const bool some = sf > 0.f;
-    const float inv = some ? __frcp_rn(sf * 0x1p100f) : 0.f;
+    const Codes8 t = encode8_tiny(w, sf);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = some ? ((i & 1) ? bf16_hi(v[i >> 1]) : bf16_lo(v[i >> 1])) * 0x1p100f : 0.f;
-      const float y = fminf(fmaxf(x * inv, -7.f), 7.f);
-      c[i] = __fsub_rn(__fadd_rn(__fadd_rn(y, kGrid), kWhole), 12582912.f);
-    }
+    for (int i = 0; i < 8; ++i) c[i] = t.c[i];
   }
   return s;
 }
@@ -128,7 +144,7 @@ __device__ __forceinline__ void store_half_mean(void* means, int flag, int64_t r
   store_mean(means, flag, rows, row, lane, make_float4(m[0], m[1], m[2], m[3]));
 }
 
-constexpr int kWriteRows = 8;  // bf16 rows in flight per lane
+constexpr int kWriteRows = 4;  // bf16 rows a lane takes at a time, the next ones in flight
 constexpr int kHeldRows = 16;  // 4-bit rows in flight per lane
 
 // Keys (kKeys) or values of two consecutive blocks of a pair, one each half of
@@ -193,11 +209,17 @@ __device__ __forceinline__ void write_blocks(const Kv4WriteParams& p, int64_t pa
   const uint8_t* src = (kKeys ? p.k_src : p.v_src) + src0 * (kHeadDim * 2) + x * 16;
   uint8_t* to = (kKeys ? p.dst.k : p.dst.v) + (row0 + held) * kCodeBytes + (kKeys ? (4 * c + g) * 4 : (8 * c + g) * 2);
   uint16_t* to_s = (kKeys ? p.dst.ks : p.dst.vs) + (row0 + held) * kGroups + g;
-  for (int r = 0; r < most; r += kWriteRows) {
-    uint4 w[kWriteRows];
+  uint4 w[kWriteRows], next[kWriteRows];
+  auto fetch = [&](int r, uint4(&to)[kWriteRows]) {  // rows r .. of the new ones, the last one where there are no more
 #pragma unroll
     for (int u = 0; u < kWriteRows; ++u)
-      w[u] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)max(min(r + u, fresh - 1), 0) * (kHeadDim * 2)));
+      to[u] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)max(min(r + u, fresh - 1), 0) * (kHeadDim * 2)));
+  };
+  fetch(0, next);
+  for (int r = 0; r < most; r += kWriteRows) {
+#pragma unroll
+    for (int u = 0; u < kWriteRows; ++u) w[u] = next[u];
+    if (r + kWriteRows < most) fetch(r + kWriteRows, next);
 #pragma unroll
     for (int u = 0; u < kWriteRows; ++u) {
       if (r + u < most) {  // warp-uniform
