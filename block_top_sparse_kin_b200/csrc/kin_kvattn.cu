@@ -64,7 +64,7 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_
 
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
       "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -74,7 +74,7 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32
 // D = A B, from zero
 __device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                             uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
       "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -83,7 +83,7 @@ __device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t
 
 __device__ __forceinline__ void mma_bf16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
       "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -574,20 +574,27 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
 #pragma unroll
         for (int G = 0; G < 4; ++G) {
           const uint4 q = lds128(q_s + G * 64);
+          float d[kStep][4];
+          uint32_t ha[kStep], hb[kStep];
 #pragma unroll
           for (int h = 0; h < kStep; ++h) {
             const uint32_t ka = part_of(wa[h], G), kb = part_of(wb[h], G);
             // the upper bytes of both halves, by the multiplier: the logic
             // unit is the busiest here
-            const uint32_t ha = __umulhi(ka, p.two24), hb = __umulhi(kb, p.two24);
+            ha[h] = __umulhi(ka, p.two24);
+            hb[h] = __umulhi(kb, p.two24);
+            mma_f16_new(d[h], ka & 0x000F000Fu, kb & 0x000F000Fu, ka & 0x00F000F0u, kb & 0x00F000F0u, q.x, q.y);
+          }
+#pragma unroll
+          for (int h = 0; h < kStep; ++h)
+            mma_f16_16816(d[h], ha[h] & 0x000F000Fu, hb[h] & 0x000F000Fu, ha[h] & 0x00F000F0u, hb[h] & 0x00F000F0u, q.z, q.w);
+#pragma unroll
+          for (int h = 0; h < kStep; ++h) {
             const float fa = __uint_as_float(part_of(sa[h], G)), fb = __uint_as_float(part_of(sb[h], G));
-            float d[4];
-            mma_f16_new(d, ka & 0x000F000Fu, kb & 0x000F000Fu, ka & 0x00F000F0u, kb & 0x00F000F0u, q.x, q.y);
-            mma_f16_16816(d, ha & 0x000F000Fu, hb & 0x000F000Fu, ha & 0x00F000F0u, hb & 0x00F000F0u, q.z, q.w);
-            s[h][0] = fmaf(fa, d[0], s[h][0]);
-            s[h][1] = fmaf(fa, d[1], s[h][1]);
-            s[h][2] = fmaf(fb, d[2], s[h][2]);
-            s[h][3] = fmaf(fb, d[3], s[h][3]);
+            s[h][0] = fmaf(fa, d[h][0], s[h][0]);
+            s[h][1] = fmaf(fa, d[h][1], s[h][1]);
+            s[h][2] = fmaf(fb, d[h][2], s[h][2]);
+            s[h][3] = fmaf(fb, d[h][3], s[h][3]);
           }
         }
       } else {
@@ -925,14 +932,19 @@ __global__ void __launch_bounds__(256) kv_weights_kernel(KvAttnParams p) {
   }
   const int t0 = (blk << lbs) + ((4 * i) & (p.bs - 1));
   float* acc = p.acc + (int64_t)pair * p.kv.Lcap + t0;
+  float w[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    if (t0 + u < L) {
-      float w = 0.f;
+    w[u] = 0.f;
 #pragma unroll
-      for (int q = 0; q < G; ++q) w += exp2f(z[u * G + q] - l[q]);
-      atomicAdd(acc + u, w);
-    }
+    for (int q = 0; q < G; ++q) w[u] += exp2f(z[u * G + q] - l[q]);
+  }
+  if (t0 + 4 <= L && (reinterpret_cast<uintptr_t>(acc) & 15u) == 0) {  // one 16-byte reduction in place of four
+    atomicAdd(reinterpret_cast<float4*>(acc), make_float4(w[0], w[1], w[2], w[3]));
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (t0 + u < L) atomicAdd(acc + u, w[u]);
   }
 }
 
