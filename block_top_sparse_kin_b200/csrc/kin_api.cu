@@ -690,11 +690,12 @@ KvSplit kv_split(const kin_dims& d, int k, bool dense) {
       best_us = us;
     }
   }
-  const int64_t slots = pairs * k;
-  const int64_t waves = (slots + wave * most - 1) / (wave * most);
+  // even ranges: whole waves of them; one may run over several short pairs
+  const int64_t slots = pairs * k, cap = k <= most ? slots : most;
+  const int64_t waves = (slots + wave * cap - 1) / (wave * cap);
   const int64_t per = (slots + wave * waves - 1) / (wave * waves);
-  if (!dense && per >= least && per < k) {
-    const double us = (double)waves * (range_us(per * tpb, kKvCtasPerSm, true) + 5.0);
+  if (!dense && per >= least && per != k && per < 2 * k) {
+    const double us = (double)waves * (range_us(per * tpb, kKvCtasPerSm, true) + 5.0 * (double)((per - 1) / k + 1));
     if (us < best_us) best = KvSplit{(int)per, k};
   }
   return best;
