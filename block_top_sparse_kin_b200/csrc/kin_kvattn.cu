@@ -164,11 +164,14 @@ __device__ __forceinline__ uint32_t tok_mask(int t, int nvalid) {
 }
 
 // A head's weights are 2^(z - r) with a reference r that follows the running
-// maximum m of its logits loosely: r = m - kLead, and m moves (all sums are
+// maximum m of its logits loosely: r = m - lead, and m moves (all sums are
 // then rescaled) only when a logit passes m + kSlack.  So a tile usually
-// costs no reduction over its tokens, and a weight is at most
-// 2^(kLead + kSlack) = 2^14, inside fp16.
-constexpr float kLead = 6.f, kSlack = 8.f;
+// costs no reduction over its tokens.  4 bit: weights reach 2^14, in the
+// middle of fp16's range.  bf16: weights stay below 1, so that values of any
+// magnitude add up.
+constexpr float kSlack = 8.f;
+template <bool kInt4>
+constexpr float kLead = kInt4 ? 6.f : -kSlack;
 
 // The sums of a warp: O^T fragments, and for its two head columns the maximum
 // logit followed, before the scaling to base 2 (raw), the reference and the
@@ -181,7 +184,7 @@ struct Acc {
 
 // The weights p of N tiles from their raw logits s (rows tq, tq + 8; heads ta,
 // ta + 1; -inf where there is no token); sl2: base-2 scale of the two heads.
-template <int N>
+template <bool kInt4, int N>
 __device__ __forceinline__ void weigh(Acc& a, const float (&s)[N][4], const float (&sl2)[2], float (&p)[N][4]) {
   float x[2] = {fmaxf(s[0][0], s[0][2]), fmaxf(s[0][1], s[0][3])};
 #pragma unroll
@@ -201,7 +204,7 @@ __device__ __forceinline__ void weigh(Acc& a, const float (&s)[N][4], const floa
       const float al = mn == a.m[j] ? 1.f : exp2_approx((a.m[j] - mn) * sl2[j]);
       a.m[j] = mn;
       a.thr[j] = mn + __fdividef(kSlack, sl2[j]);
-      a.r[j] = mn * sl2[j] - kLead;
+      a.r[j] = mn * sl2[j] - kLead<kInt4>;
       a.l[j] *= al;
       a.sums[j] *= al;
       a.sums[2 + j] *= al;
@@ -453,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
     *reinterpret_cast<uint4*>(s_q + hd * 64 + x * 4) =
         make_uint4(pack_f16x2(x0, x1), pack_f16x2(x2 * 0x1p-4f, x3 * 0x1p-4f), pack_f16x2(x4, x5), pack_f16x2(x6 * 0x1p-4f, x7 * 0x1p-4f));
     if ((x & 3) == 0) s_off[hd][x >> 2] = sum * -0x1p-21f;  // -8 * 2^-24
-    if (x == 0) s_sl2[hd] = p.scale_log2 * __uint_as_float(min(278u - fe, 254u) << 23);  // 2^24 / f
+    // 2^24 / f; infinity where q passes 2^118 and it overflows: the outputs are then not finite
+    if (x == 0) s_sl2[hd] = p.scale_log2 * __uint_as_float(min(278u - fe, 255u) << 23);
     __syncthreads();
     sl2[0] = s_sl2[ta];
     sl2[1] = s_sl2[ta + 1];
@@ -647,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
           }
         }
       }
-      weigh(a, s, sl2, pr);
+      weigh<kInt4>(a, s, sl2, pr);
       if constexpr (kInt4) {
 #pragma unroll
         for (int h = 0; h < kStep; ++h) {

@@ -396,6 +396,55 @@ def test_attention(case, paged, int4):
 
 
 @pytest.mark.parametrize("int4", [True, False], ids=["int4", "bf16"])
+@pytest.mark.parametrize("B,k", [(64, 128), (32, 256), (61, 10), (3, 129)])
+def test_attention_ranges_over_many_pairs(B, k, int4):
+    """Ragged batches that fill the card: ranges that run over one pair's end
+    into the next, over several short pairs, and pairs of one range each; some
+    pairs keep fewer blocks than the budget, one sequence is empty."""
+    lens = [(1 + 37 * i * i) % 4300 for i in range(B)]
+    lens[1], lens[2], lens[-1] = 0, 1, 4300
+    c = Cache(lens, 8, 16, 4300, True, 65)
+    g = 2
+    kv, d, st = (c.stored() if int4 else c.bf16()), c.dims(g), status()
+    q = rows16(66, B, 8 * g, D)
+    sel, cnt = random_selection(c, k, 67)
+    out, lse = torch.full_like(q, 9.0), torch.full((B, 8 * g), 9.0, device="cuda")
+    acc = torch.zeros((B, 8, 4300), device="cuda")
+    ws = kin.alloc_kv_attn_workspace(d, k, acc=True)
+    for _ in range(2):  # the second call meets the first one's workspace
+        acc.zero_()
+        kin.kin_kv_decode_attn(d, q, kv, c.seq, sel.cuda(), cnt.cuda(), k, 0.0, out, lse, ws, acc=acc, dev_status=st)
+        check_attention(c, q, out, lse, acc, None, int4, sel.tolist())
+    assert int(st.item()) == 5  # the empty sequence
+
+
+def test_attention_bf16_values_of_any_magnitude():
+    """Weights below 1: the largest finite values average without overflow."""
+    c = Cache([300], 1, 16, 300, False, 68)
+    c.v = (c.v.float().clamp(-1, 1) * 3e38).to(torch.bfloat16)
+    q = rows16(69, 1, 2, D)
+    out, lse, d = torch.empty_like(q), torch.empty((1, 2), device="cuda"), c.dims(2)
+    kin.kin_kv_decode_attn(d, q, c.bf16(), c.seq, None, None, 0, 0.0, out, lse, kin.alloc_kv_attn_workspace(d, 0))
+    check_attention(c, q, out, lse, None, None, False)
+
+
+def test_attention_queries_of_any_magnitude():
+    """Each head's queries are scaled on their own: tiny beside huge ones, and zeros."""
+    c = Cache([120], 1, 16, 120, False, 70)
+    q = rows16(71, 1, 6, D).float()
+    q *= torch.tensor([1, 2.0**-40, 2.0**40, 0, 2.0**-126, 2.0**100], device="cuda")[None, :, None]
+    q = q.to(torch.bfloat16)
+    c.k[:, :, :, :] *= 2.0**-7
+    out, lse, d = torch.empty_like(q), torch.empty((1, 6), device="cuda"), c.dims(6)
+    hk, hv = c.held()
+    for j, scale in enumerate([0.2, 2.0**39, 2.0**-41, 0.2, 0.2, 2.0**-102]):
+        kin.kin_kv_decode_attn(d, q, c.stored(), c.seq, None, None, 0, scale, out, lse, kin.alloc_kv_attn_workspace(d, 0))
+        o, l, _, _ = ref.attend(q, hk, hv, [120], None, scale, 16)
+        assert abs(float(lse[0, j]) - float(l[0, j])) < 1e-4
+        assert (out[0, j].double() - o[0, j]).abs().max() < 2.0**-7 * o[0, j].abs().max()
+
+
+@pytest.mark.parametrize("int4", [True, False], ids=["int4", "bf16"])
 def test_attention_empty_and_bad_sequences(int4):
     """Lengths of 0 and beyond the capacity and pairs that keep nothing: out 0,
     lse -inf, weights untouched; a block listed beyond the length is left out."""
