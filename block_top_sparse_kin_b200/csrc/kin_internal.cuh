@@ -326,10 +326,7 @@ struct TokenParams {
 // A cache as kin_kv describes it.  INT4 rows: kCodeBytes bytes of codes and
 // kGroups bf16 scales, one per kGroupDim channels (see kin.h).
 constexpr int kGroupDim = 32;
-#ifndef KIN_KV_CTAS_PER_SM
-#define KIN_KV_CTAS_PER_SM 3
-#endif
-constexpr int kKvCtasPerSm = KIN_KV_CTAS_PER_SM;  // resident CTAs of the attention
+constexpr int kKvCtasPerSm = 3;  // resident CTAs of the attention
 constexpr int kKvItemTiles = 256;  // attention tiles per CTA and pair (64 per warp, two per lane)
 constexpr int kGroups = kHeadDim / kGroupDim;
 constexpr int kCodeBytes = kHeadDim / 2;

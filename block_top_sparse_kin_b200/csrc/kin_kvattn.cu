@@ -13,10 +13,18 @@
 //   sum_t p_t V_td = sum_t (p_t vs_tg) c_td  the scale goes to the weight
 // so the codes enter the matrix instructions exactly and no row is rounded.
 //
-// Bounded by HBM: 144 bytes (4 bit) or 512 bytes (bf16) a token and pair
-// against 4 g D flops.  A decode group has at most 8 heads, so the products
-// are mma.sync m16n8k16 tiles of 16 tokens by 8 heads, fed per warp by a
-// ring of asynchronous copies.
+// A decode group has at most 8 heads, so the products are mma.sync m16n8k16
+// tiles of 16 tokens by 8 heads, fed per warp by a ring of asynchronous
+// copies, 3 CTAs of 4 warps on an SM.  The bytes, 144 (4 bit) or 512 (bf16) a
+// token and pair, bound bf16 rows: 32 x 8 pairs, 4096 of 32768 tokens each, 4
+// heads: 88 us, 6.1 TB/s.  4-bit rows are bounded by what a tile costs the
+// SM: the same batch 41.6 us, 3.6 TB/s; about 230 instructions a tile and
+// warp, 100 of them for the logic unit (64 unpack its 4096 codes), none of the
+// units over 60% busy, so warps wait on one another's bursts.  Measured on the
+// way there: nibbles through one conversion for two, 66 us; as fp16
+// subnormals, with no conversion, 49; two tiles a step, which share the
+// maximum, the copies' waits and the query loads, and even ranges, 42.  16
+// warps of 128 registers, one tile a step: 45.
 #include "kin_internal.cuh"
 
 namespace kin {
@@ -25,30 +33,21 @@ namespace {
 
 #define kNegInf (-__int_as_float(0x7f800000))
 
-#ifndef KIN_KV4_STEP
-#define KIN_KV4_STEP 2
-#endif
-#ifndef KIN_KV4_STAGES
-#define KIN_KV4_STAGES 3
-#endif
-#ifndef KIN_KV_WARPS
-#define KIN_KV_WARPS 4
-#endif
-constexpr int kWarps = KIN_KV_WARPS;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kDims = kHeadDim / kThreads;  // output channels of a thread
+static_assert(kThreads == kHeadDim, "a thread has one output channel, and 16 threads a query head");
 constexpr int kRowPad = kHeadDim + 4;
 constexpr int kHalfBox = 16 * 64 * 2;
 
 template <bool kInt4>
 struct Ring {
   // tiles of 16 tokens that a warp takes at a step
-  static constexpr int kStep = kInt4 ? KIN_KV4_STEP : 1;
+  static constexpr int kStep = kInt4 ? 2 : 1;
   // bf16: K0 K1 V0 V1 half tiles of 16 rows x 64 channels.  4 bit: 16 rows of
   // 64 bytes of key codes, of value codes, then 16 x 4 scales of each.
   static constexpr int kTileBytes = kInt4 ? 2 * 16 * kCodeBytes + 2 * 16 * kGroups * 2 : 4 * kHalfBox;
   static constexpr int kStageBytes = kStep * kTileBytes;
-  static constexpr int kStages = kInt4 ? KIN_KV4_STAGES : 2;
+  static constexpr int kStages = kInt4 ? 3 : 2;
   // 4 bit, per warp and tile behind the ring: the tile's key scales as fp32
   // [16][4] and its value scales as fp16 pairs [8 token pairs][4]
   static constexpr int kScaleBytes = kInt4 ? 256 + 128 : 0;
@@ -788,19 +787,16 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
     if (nchunks == 1) write_lse(j, den, M);
   }
   __syncthreads();
-  auto combined = [&](int j, int d) {
+  auto combined = [&](int j) {
     float num = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) num += s_ww[w][j] * comb[(w * kMaxGroup + j) * kRowPad + d];
+    for (int w = 0; w < kWarps; ++w) num += s_ww[w][j] * comb[(w * kMaxGroup + j) * kRowPad + tid];
     return num;
   };
-  auto finish = [&](int j, int d, float num) { p.out[(qh0 + j) * kHeadDim + d] = __float2bfloat16_rn(num * s_inv[j]); };
+  auto finish = [&](int j, float num) { p.out[(qh0 + j) * kHeadDim + tid] = __float2bfloat16_rn(num * s_inv[j]); };
   if (nchunks == 1) {
 #pragma unroll 2
-    for (int j = 0; j < g; ++j) {
-#pragma unroll
-      for (int i = 0; i < kDims; ++i) finish(j, tid + kThreads * i, combined(j, tid + kThreads * i));
-    }
+    for (int j = 0; j < g; ++j) finish(j, combined(j));
     __syncthreads();  // the next pair's ring takes the combine area
     continue;
   }
@@ -809,8 +805,7 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   float* part = p.partials + ((int64_t)pair * p.max_chunks + chunk) * g * kPartStride;
 #pragma unroll 1
   for (int j = 0; j < g; ++j) {
-#pragma unroll
-    for (int i = 0; i < kDims; ++i) part[j * kPartStride + tid + kThreads * i] = combined(j, tid + kThreads * i);
+    part[j * kPartStride + tid] = combined(j);
     if (tid == 0) {
       part[j * kPartStride + kHeadDim] = s_cm[j];
       part[j * kPartStride + kHeadDim + 1] = s_cden[j];
@@ -831,12 +826,9 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   const float4* src4 = reinterpret_cast<const float4*>(p.partials + (int64_t)pair * p.max_chunks * rec);
   const float* stage = reinterpret_cast<const float*>(smem);
   const uint32_t stage_s = smem_u32(smem);
-  float num[kMaxGroup][kDims];
+  float num[kMaxGroup];
 #pragma unroll
-  for (int j = 0; j < kMaxGroup; ++j) {
-#pragma unroll
-    for (int i = 0; i < kDims; ++i) num[j][i] = 0.f;
-  }
+  for (int j = 0; j < kMaxGroup; ++j) num[j] = 0.f;
   if (tid < g) {
     s_mr[tid] = kNegInf;
     s_den[tid] = 0.f;
@@ -871,22 +863,14 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kMaxGroup; ++j) {
-      if (j < g) {
-#pragma unroll
-        for (int i = 0; i < kDims; ++i) num[j][i] *= s_a[j];
-      }
-    }
+    for (int j = 0; j < kMaxGroup; ++j)
+      if (j < g) num[j] *= s_a[j];
 #pragma unroll 2
     for (int cc = 0; cc < nbat; ++cc) {
       const float* rc = stage + cc * g * kPartStride + tid;
 #pragma unroll
-      for (int j = 0; j < kMaxGroup; ++j) {
-        if (j < g) {
-#pragma unroll
-          for (int i = 0; i < kDims; ++i) num[j][i] += s_w[cc * g + j] * rc[j * kPartStride + kThreads * i];
-        }
-      }
+      for (int j = 0; j < kMaxGroup; ++j)
+        if (j < g) num[j] += s_w[cc * g + j] * rc[j * kPartStride];
     }
     __syncthreads();  // the next batch overwrites the staging area and the weights
   }
@@ -894,10 +878,7 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kMaxGroup; ++j)
-    if (j < g) {
-#pragma unroll
-      for (int i = 0; i < kDims; ++i) finish(j, tid + kThreads * i, num[j][i]);
-    }
+    if (j < g) finish(j, num[j]);
   }
 }
 
