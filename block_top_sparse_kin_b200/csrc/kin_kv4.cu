@@ -175,6 +175,7 @@ __device__ __forceinline__ void write_blocks(const Kv4WriteParams& p, int64_t pa
     if (row0 < 0 || src0 < 0) {  // a page index outside its pool: the block is left as it was
       if (kKeys) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
       t1 = t0;
+      row0 = src0 = 0;  // a half without rows reads row 0 beside the other's
     }
   }
   const int held = t0 < t1 ? tn - t0 : 0, fresh = t0 < t1 ? t1 - tn : 0;
@@ -215,7 +216,7 @@ __device__ __forceinline__ void write_blocks(const Kv4WriteParams& p, int64_t pa
     for (int u = 0; u < kWriteRows; ++u)
       to[u] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)max(min(r + u, fresh - 1), 0) * (kHeadDim * 2)));
   };
-  fetch(0, next);
+  if (most > 0) fetch(0, next);
   for (int r = 0; r < most; r += kWriteRows) {
 #pragma unroll
     for (int u = 0; u < kWriteRows; ++u) w[u] = next[u];
@@ -419,6 +420,7 @@ __device__ __forceinline__ void move_blocks(const EvictParams& p, int64_t pair, 
     if (to0 < 0) {
       if (kKeys) set_status(p.dev_status, KIN_ERR_DEVICE_DATA);
       n = 0;
+      to0 = 0;
     }
   }
   const int most = max(n, __shfl_xor_sync(0xffffffffu, n, 16));

@@ -255,8 +255,9 @@ def test_append_nothing_and_without_room():
     kv, st = c.stored(), status()
     out = torch.full((3,), -1, dtype=torch.int32, device="cuda")
     new = rows16(5, 3, 1, 4, D)
-    kin.kin_kv4_append(c.dims(), kv, None, c.seq, out, new, new, 0, st)
+    kin.kin_kv4_append(c.dims(), kv, None, c.seq, out, new[:1, :, :1, :8].contiguous(), new, 0, st)  # nothing is read of it
     assert out.tolist() == [3, 16, 9] and int(st.item()) == 0
+    c.check4(kv)
     kin.kin_kv4_append(c.dims(), kv, None, c.seq, out, new, new, 4, st)  # the second has no room
     assert out.tolist() == [7, 16, 13] and int(st.item()) == 5
     got = kv.k[1, 0]
