@@ -178,6 +178,15 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None, nullable=False, count
     raise ValueError(f"{name} holds {t.numel()} elements; the dims need {count}")
 
 
+def _ptr(t, name: str, dtype, count, dev: int):
+    """_dev for the common case, at a third of its cost: a contiguous tensor
+    of one dtype on the current device `dev`."""
+    if (t is not None and count is not None and t.get_device() == dev and t.dtype is dtype and t.numel() >= count
+            and t.is_contiguous()):
+        return t.data_ptr()
+    return _dev(t, name, _BF16 if dtype is torch.bfloat16 else dtype, count=count)
+
+
 class _Counts:
     """Element counts of every buffer a call touches, from the dims (all
     None when the dims are invalid: the call then returns the library's
@@ -199,6 +208,7 @@ class _Counts:
         self.page = Hkv * bs * D if ok else None       # one page of a pool
         self.page_mean = Hkv * D if ok else None       # one per-page mean
         self.bkd = B * Hkv * D if ok else None         # one appended row per (b, h)
+        self.rows = B * Hkv * L if ok else None        # tokens of the cache (accumulated weights)
 
     def times(self, n, per):
         return None if per is None else int(n) * per
@@ -554,22 +564,22 @@ class KvCache:
                              _dev(self._v, f"{name}.v", rows), *scales)
             self._at = [t.data_ptr() for t in self._tensors()]
             self._device = _current_device()
+        k, v, ks, vs, table, at = self._k, self._v, self._k_scales, self._v_scales, self._block_table, self._at
         if self._device != _current_device():
             raise ValueError(f"{name} is on cuda:{self._device}; the calls run on the current device")
-        if [t.data_ptr() for t in self._tensors()] != self._at:
+        if (k.data_ptr() != at[0] or v.data_ptr() != at[1] or (ks is not None and (ks.data_ptr() != at[2] or vs.data_ptr() != at[3]))
+                or (table is not None and table.data_ptr() != at[-1])):
             raise ValueError(f"{name}: a tensor of the cache has moved since its first call")
         if c.ok:
-            elements = c.cache if self._block_table is None else self._c.num_pages * c.page
-            if self._k_scales is None:
-                sizes = ((self._k, elements, "k"), (self._v, elements, "v"))
+            need = c.cache if table is None else self._c.num_pages * c.page
+            if ks is None:
+                fits = k.numel() >= need and v.numel() >= need
             else:
-                sizes = ((self._k, elements >> 1, "k"), (self._v, elements >> 1, "v"),
-                         (self._k_scales, elements >> 5, "k_scales"), (self._v_scales, elements >> 5, "v_scales"))
-            for t, need, of in sizes:
-                if t.numel() < need:
-                    raise ValueError(f"{name}.{of} holds {t.numel()} elements; the dims need {need}")
-            if self._block_table is not None and self._block_table.numel() < c.table:
-                raise ValueError(f"{name}.block_table holds {self._block_table.numel()} elements; the dims need {c.table}")
+                codes, scales = need >> 1, need >> 5
+                fits = k.numel() >= codes and v.numel() >= codes and ks.numel() >= scales and vs.numel() >= scales
+            if not fits or (table is not None and table.numel() < c.table):
+                raise ValueError(f"{name}: a tensor of the cache is smaller than the dims need ({need} channels in k and in v"
+                                 + (f", {c.table} table entries)" if table is not None else ")"))
         return self._c, self._c.num_pages
 
 
@@ -614,12 +624,15 @@ def kin_kv4_append(dims, kv: KvCache, block_means, seq_lens, new_lens, k_new, v_
     """n_new tokens onto a 4-bit cache; new_lens may be seq_lens (in place)."""
     c = _counts(dims)
     d, pages = kv._struct(c, "kv")
+    dev = _current_device()
     means, dtype = _kv_means(block_means, c, dims, pages, per_page)
-    new_rows = c.times(max(int(n_new), 0), c.bkd)
+    n = int(n_new)
+    new_rows = c.times(max(n, 0), c.bkd)
+    i32, bf16 = torch.int32, torch.bfloat16
     rc = load_library().kin_kv4_append(
-        ctypes.byref(dims), ctypes.byref(d), means, dtype, _dev(seq_lens, "seq_lens", torch.int32, count=c.lens),
-        _dev(new_lens, "new_lens", torch.int32, count=c.lens), _dev(k_new, "k_new", _BF16, count=new_rows),
-        _dev(v_new, "v_new", _BF16, count=new_rows), int(n_new), _status(dev_status), _stream(stream))
+        ctypes.byref(dims), ctypes.byref(d), means, dtype, _ptr(seq_lens, "seq_lens", i32, c.lens, dev),
+        _ptr(new_lens, "new_lens", i32, c.lens, dev), _ptr(k_new, "k_new", bf16, new_rows, dev),
+        _ptr(v_new, "v_new", bf16, new_rows, dev), n, _status(dev_status), _stream(stream))
     _check(rc, "kin_kv4_append")
 
 
@@ -628,12 +641,14 @@ def kin_kv4_load(dims, kv: KvCache, seq_lens, k_out, v_out, starts=None, n=None,
     not given) into k_out / v_out [B, Hkv, n, D]; n defaults to k_out's."""
     c = _counts(dims)
     d, _ = kv._struct(c, "kv")
+    dev = _current_device()
     n = int(k_out.shape[2]) if n is None else int(n)
     rows = c.times(max(n, 0), c.bkd)
+    i32, bf16 = torch.int32, torch.bfloat16
     rc = load_library().kin_kv4_load(
-        ctypes.byref(dims), ctypes.byref(d), _dev(seq_lens, "seq_lens", torch.int32, count=c.lens),
-        _dev(starts, "starts", torch.int32, nullable=True, count=c.lens), n, _dev(k_out, "k_out", _BF16, count=rows),
-        _dev(v_out, "v_out", _BF16, count=rows), _status(dev_status), _stream(stream))
+        ctypes.byref(dims), ctypes.byref(d), _ptr(seq_lens, "seq_lens", i32, c.lens, dev),
+        None if starts is None else _ptr(starts, "starts", i32, c.lens, dev), n, _ptr(k_out, "k_out", bf16, rows, dev),
+        _ptr(v_out, "v_out", bf16, rows, dev), _status(dev_status), _stream(stream))
     _check(rc, "kin_kv4_load")
 
 
@@ -656,15 +671,15 @@ def kin_kv_decode_attn(dims, q, kv: KvCache, seq_lens, sel_idx, sel_cnt, k_block
     attention weights on top of what it holds."""
     c = _counts(dims)
     d, _ = kv._struct(c, "kv")
+    dev = _current_device()
     k = int(k_blocks)
-    acc_rows = None if c.cache is None else c.cache // dims.head_dim
+    i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
     rc = load_library().kin_kv_decode_attn(
-        ctypes.byref(dims), _dev(q, "q", _BF16, count=c.q), ctypes.byref(d),
-        _dev(seq_lens, "seq_lens", torch.int32, count=c.lens),
-        _dev(sel_idx, "sel_idx", torch.int32, nullable=True, count=c.times(max(k, 0), c.pairs)),
-        _dev(sel_cnt, "sel_cnt", torch.int32, nullable=True, count=c.pairs), k, float(softmax_scale),
-        _dev(out, "out", _BF16, count=c.q), _dev(lse, "lse", torch.float32, nullable=True, count=c.lse),
-        _dev(acc, "acc", torch.float32, nullable=True, count=acc_rows), _dev(workspace, "workspace"),
+        ctypes.byref(dims), _ptr(q, "q", bf16, c.q, dev), ctypes.byref(d), _ptr(seq_lens, "seq_lens", i32, c.lens, dev),
+        None if sel_idx is None else _ptr(sel_idx, "sel_idx", i32, c.times(max(k, 0), c.pairs), dev),
+        None if sel_cnt is None else _ptr(sel_cnt, "sel_cnt", i32, c.pairs, dev), k, float(softmax_scale),
+        _ptr(out, "out", bf16, c.q, dev), None if lse is None else _ptr(lse, "lse", f32, c.lse, dev),
+        None if acc is None else _ptr(acc, "acc", f32, c.rows, dev), _dev(workspace, "workspace"),
         workspace.numel() * workspace.element_size(), _status(dev_status), _stream(stream))
     _check(rc, "kin_kv_decode_attn")
 
@@ -687,15 +702,14 @@ def kin_kv_evict(dims, kv: KvCache, acc, seq_lens, n_keep, n_sink, n_recent, dst
     c, cd = _counts(dims), _counts(dst_dims)
     s, _ = kv._struct(c, "kv")
     d, pages = dst._struct(cd, "dst")
+    dev = _current_device()
     means, dtype = _kv_means(block_means, cd, dst_dims, pages, per_page)
-    rows = None if c.cache is None else c.cache // dims.head_dim
-    dst_rows = None if cd.cache is None else cd.cache // dst_dims.head_dim
+    i32, f32, keep = torch.int32, torch.float32, int(n_keep)
     rc = load_library().kin_kv_evict(
-        ctypes.byref(dims), ctypes.byref(s), _dev(acc, "acc", torch.float32, count=rows),
-        _dev(seq_lens, "seq_lens", torch.int32, count=c.lens), int(n_keep), int(n_sink), int(n_recent),
-        ctypes.byref(dst_dims), ctypes.byref(d), _dev(dst_acc, "dst_acc", torch.float32, nullable=True, count=dst_rows),
-        _dev(dst_lens, "dst_lens", torch.int32, count=c.lens), means, dtype,
-        _dev(sel_tokens, "sel_tokens", torch.int32, nullable=True, count=c.times(max(int(n_keep), 0), c.pairs)),
-        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _status(dev_status),
-        _stream(stream))
+        ctypes.byref(dims), ctypes.byref(s), _ptr(acc, "acc", f32, c.rows, dev), _ptr(seq_lens, "seq_lens", i32, c.lens, dev),
+        keep, int(n_sink), int(n_recent), ctypes.byref(dst_dims), ctypes.byref(d),
+        None if dst_acc is None else _ptr(dst_acc, "dst_acc", f32, cd.rows, dev), _ptr(dst_lens, "dst_lens", i32, c.lens, dev),
+        means, dtype,
+        None if sel_tokens is None else _ptr(sel_tokens, "sel_tokens", i32, c.times(max(keep, 0), c.pairs), dev),
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _status(dev_status), _stream(stream))
     _check(rc, "kin_kv_evict")
