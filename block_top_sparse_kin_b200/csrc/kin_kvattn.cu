@@ -57,8 +57,23 @@ struct Ring {
   static constexpr int kSmem = (kPipe > kComb ? kPipe : kComb) + 1024;
 };
 
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+// Rows are read once: their lines leave L2 before the logits and partials do.
+__device__ __forceinline__ uint64_t read_once_policy() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+__device__ __forceinline__ void cp_async16_once(uint32_t dst, const void* src, uint32_t src_bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(src_bytes),
+               "l"(policy)
+               : "memory");
+}
+
+__device__ __forceinline__ void cp_async8_once(uint32_t dst, const void* src, uint32_t src_bytes, uint64_t policy) {
+  asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], 8, %2, %3;" ::"r"(dst), "l"(src), "r"(src_bytes),
+               "l"(policy)
+               : "memory");
 }
 
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -352,17 +367,18 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   }
   __syncwarp();
 
+  const uint64_t once = read_once_policy();
   auto issue_tile = [&](int nt, uint32_t row, uint32_t slot) {  // slot: byte offset of the tile's place in the ring
     if (row < kPartial) {
       if constexpr (kInt4) {
         const uint8_t* ks = p.kv.k + (uint64_t)row * kCodeBytes + lane * 16;
         const uint8_t* vs = p.kv.v + (uint64_t)row * kCodeBytes + lane * 16;
         const uint16_t* ss = (lane < 16 ? p.kv.ks : p.kv.vs) + ((uint64_t)row + (lane & 15)) * kGroups;
-        cp_async16(code_dst + slot, ks, 16u);
-        cp_async16(code_dst + slot + 512, ks + 512, 16u);
-        cp_async16(code_dst + slot + 1024, vs, 16u);
-        cp_async16(code_dst + slot + 1536, vs + 512, 16u);
-        cp_async8(scale_dst + slot, ss, 8u);
+        cp_async16_once(code_dst + slot, ks, 16u, once);
+        cp_async16_once(code_dst + slot + 512, ks + 512, 16u, once);
+        cp_async16_once(code_dst + slot + 1024, vs, 16u, once);
+        cp_async16_once(code_dst + slot + 1536, vs + 512, 16u, once);
+        cp_async8_once(scale_dst + slot, ss, 8u, once);
       } else {
         const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.kv.k) + (uint64_t)row * kHeadDim;
         const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.kv.v) + (uint64_t)row * kHeadDim;
@@ -371,8 +387,8 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
           const int piece = lane + 32 * i;
           const int r = piece >> 4, cc = piece & 15;
           const uint32_t off = ring + slot + (uint32_t)((cc >> 3) * kHalfBox + r * 128 + (((cc & 7) ^ (r & 7)) << 4));
-          cp_async16(off, k + piece * 8, 16u);
-          cp_async16(off + 2 * kHalfBox, v + piece * 8, 16u);
+          cp_async16_once(off, k + piece * 8, 16u, once);
+          cp_async16_once(off + 2 * kHalfBox, v + piece * 8, 16u, once);
         }
       }
     } else {  // rows behind the length: zeros, nothing read (the address stays on a valid row)
@@ -386,13 +402,13 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
           for (int i = 0; i < 2; ++i) {
             const int t = tq + 8 * i;
             const int64_t from = (int64_t)row * kCodeBytes + lane * 16 + (t < nv ? 512 * i : -tq * 64);
-            cp_async16(code_dst + slot + 512 * i, p.kv.k + from, t < nv ? 16u : 0u);
-            cp_async16(code_dst + slot + 1024 + 512 * i, p.kv.v + from, t < nv ? 16u : 0u);
+            cp_async16_once(code_dst + slot + 512 * i, p.kv.k + from, t < nv ? 16u : 0u, once);
+            cp_async16_once(code_dst + slot + 1024 + 512 * i, p.kv.v + from, t < nv ? 16u : 0u, once);
           }
         }
         const int t = lane & 15;
-        cp_async8(scale_dst + slot, (lane < 16 ? p.kv.ks : p.kv.vs) + ((uint64_t)row + (t < nv ? t : 0)) * kGroups,
-                  t < nv ? 8u : 0u);
+        cp_async8_once(scale_dst + slot, (lane < 16 ? p.kv.ks : p.kv.vs) + ((uint64_t)row + (t < nv ? t : 0)) * kGroups,
+                       t < nv ? 8u : 0u, once);
       } else if (nv > 0) {
         const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.kv.k) + (uint64_t)row * kHeadDim;
         const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.kv.v) + (uint64_t)row * kHeadDim;
@@ -403,8 +419,8 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
           const uint32_t off = ring + slot + (uint32_t)((cc >> 3) * kHalfBox + r * 128 + (((cc & 7) ^ (r & 7)) << 4));
           const int src = (r < nv ? r : 0) * kHeadDim + cc * 8;
           const uint32_t bytes = r < nv ? 16u : 0u;
-          cp_async16(off, k + src, bytes);
-          cp_async16(off + 2 * kHalfBox, v + src, bytes);
+          cp_async16_once(off, k + src, bytes, once);
+          cp_async16_once(off + 2 * kHalfBox, v + src, bytes, once);
         }
       }
     }
