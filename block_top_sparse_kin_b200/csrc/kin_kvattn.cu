@@ -18,9 +18,9 @@
 // copies, 3 CTAs of 4 warps on an SM.  The bytes, 144 (4 bit) or 512 (bf16) a
 // token and pair, bound bf16 rows: 32 x 8 pairs, 4096 of 32768 tokens each, 4
 // heads: 87 us, 6.2 TB/s.  4-bit rows are bounded by what a tile costs the
-// SM: the same batch 41 us, 3.7 TB/s; about 230 instructions a tile and
-// warp, 100 of them for the logic unit (64 unpack its 4096 codes), none of the
-// units over 60% busy, so warps wait on one another's bursts.  Measured on the
+// SM: the same batch 41 us, 3.7 TB/s; 249 instructions a tile by
+// one warp, 102 of them for the logic unit (64 unpack its 4096 codes), no unit
+// over half busy, so warps wait on one another's bursts.  Measured on the
 // way there: nibbles through one conversion for two, 66 us; as fp16
 // subnormals, with no conversion, 49; two tiles a step, which share the
 // maximum, the copies' waits and the query loads, and even ranges, 42.  16
