@@ -58,6 +58,10 @@ struct Ring {
 };
 
 // Rows are read once: their lines leave L2 before the logits and partials do.
+// 32 x 8 pairs of 4096 tokens, against copies without the hint: bf16 rows 86.4
+// us for 89.5, 4-bit rows 40.7 for 41.9; with weights 52.5 for 53.4 (4 bit) and
+// 102.5 for 103.1 (bf16), three caches in turn.  Called on one cache again and
+// again, bf16 with weights takes 95 for 103.
 __device__ __forceinline__ uint64_t read_once_policy() {
   uint64_t p;
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
