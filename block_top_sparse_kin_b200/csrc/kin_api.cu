@@ -1,6 +1,7 @@
 // kin_api.cu -- the extern "C" boundary of libkin.so: argument checks,
 // workspace layout, launch-shape heuristics and launches.
 // Semantics of every call are documented in include/kin.h.
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <cmath>
@@ -656,8 +657,14 @@ bool same_cache(const KvView& a, const KvView& b) { return a.k == b.k || a.v == 
 // blocks, one per CTA.  A pair's slots are padded to `stride`: a multiple of
 // per (aligned: no range crosses a pair), or k itself (ranges that run on into
 // the next pair, so that every resident CTA gets the same).
+// fit, in a dense call whose ranges all are resident at once: the kernel, which
+// knows the lengths, cuts each pair into ranges of fit (32 tiles, chosen so
+// that short sequences leave few partials; not swept) to per blocks.  8 pairs, 8 heads,
+// a cache of 128K tokens that holds 8K: 17.1 us, 31.9 with the capacity's
+// ranges; 128 pairs, 2000 of 8192 tokens: 17.6 for 28.8; calls of a few short
+// sequences take 0.2 us more.
 struct KvSplit {
-  int per, stride;
+  int per, stride, fit;
 };
 
 // Chosen by an estimate in microseconds, from timings of 4-bit caches (bf16
@@ -676,19 +683,29 @@ KvSplit kv_split(const kin_dims& d, int k, bool dense) {
   auto range_us = [&](int64_t tiles, int64_t per_sm, bool merged) {
     return (double)tiles * (per_sm <= 1 ? 0.109 : per_sm == 2 ? 0.149 : 0.216) + (merged ? 5.0 : 4.0);
   };
-  KvSplit best{0, 0};
+  KvSplit best{0, 0, 0};
   double best_us = 0;
-  const int c0 = (k + most - 1) / most;
-  for (int c = c0; c < c0 + 64; ++c) {
-    const int per = (k + c - 1) / c;
-    if (c > c0 && per < least) break;
+  auto consider = [&](int per) {
     const int64_t n = pairs * ((k + per - 1) / per), full = n / wave, rest = n % wave;
     double us = (double)full * range_us((int64_t)per * tpb, kKvCtasPerSm, per < k);
     if (rest) us += range_us((int64_t)per * tpb, (rest + kTargetSMs - 1) / kTargetSMs, per < k);
     if (!best.per || us < best_us) {
-      best = KvSplit{per, (k + per - 1) / per * per};
+      best = KvSplit{per, (k + per - 1) / per * per, 0};
       best_us = us;
     }
+  };
+  const int c0 = (k + most - 1) / most;
+  for (int c = c0; c < c0 + 64; ++c) {
+    const int per = (k + c - 1) / c;
+    if (c > c0 && per < least) break;
+    consider(per);
+  }
+  // dense: longer ranges where one wave holds them all, none waits for another
+  // (8 pairs of 128K tokens, 8 heads: 50 us, 72 in ranges of 128 tiles or less;
+  // 128 pairs of 8192: 42 for 46.5; the same of bf16 rows, 4 heads: 84 for 83.5)
+  if (dense && pairs <= wave) {
+    const int c = (int)(wave / pairs), per = (k + c - 1) / c;
+    if (per > most && per <= kKvItemTiles / tpb) consider(per);
   }
   // even ranges: whole waves of them; one may run over several short pairs
   const int64_t slots = pairs * k, cap = k <= most ? slots : most;
@@ -696,8 +713,9 @@ KvSplit kv_split(const kin_dims& d, int k, bool dense) {
   const int64_t per = (slots + wave * waves - 1) / (wave * waves);
   if (!dense && per >= least && per != k && per < 2 * k) {
     const double us = (double)waves * (range_us(per * tpb, kKvCtasPerSm, true) + 5.0 * (double)((per - 1) / k + 1));
-    if (us < best_us) best = KvSplit{(int)per, k};
+    if (us < best_us) best = KvSplit{(int)per, k, 0};
   }
+  if (dense && pairs * (best.stride / best.per) <= wave) best.fit = std::min(best.per, (32 + tpb - 1) / tpb);
   return best;
 }
 
@@ -869,6 +887,7 @@ KIN_EXPORT kin_status kin_kv_decode_attn(const kin_dims* dims, const void* q, co
   p.k = kv_slots(*dims, k_blocks);
   p.per = split.per;
   p.stride = split.stride;
+  p.fit = split.fit;
   if ((int64_t)pairs_of(*dims) * p.stride >= (int64_t)1 << 31) return KIN_ERR_CAPACITY;
   p.slots = pairs_of(*dims) * p.stride;
   p.max_chunks = kv_max_chunks(p.k, split);

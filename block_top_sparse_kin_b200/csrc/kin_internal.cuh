@@ -400,6 +400,7 @@ struct KvAttnParams {
   int stride;              // a pair's slots: k, or padded to a multiple of per
   int slots;               // pairs x stride
   int per;                 // slots of a CTA
+  int fit;                 // not 0: ranges cut by the length instead, at least this, at most per
   int max_chunks;          // CTAs that a pair's slots may meet
   float scale_log2;
   uint32_t two24;          // 2^24, where the kernel cannot see its value

@@ -298,10 +298,17 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   // blocks [j0, j1) of one pair at a time.
   const int hi_slot = min((int)(blockIdx.x + 1) * p.per, p.slots);
   for (int at = blockIdx.x * p.per; at < hi_slot;) {
-  const int pair = at / p.stride, j0 = at - pair * p.stride;
-  const int j1 = min(p.k, hi_slot - pair * p.stride);
+  const int pair = at / p.stride;
+  int j0 = at - pair * p.stride, j1 = min(p.k, hi_slot - pair * p.stride), per = p.per;
   at = (pair + 1) * p.stride;
   const int b = pair / p.Hkv, h = pair - b * p.Hkv;
+  const int L = __ldg(p.seq_lens + b);
+  if (p.fit) {  // dense, every CTA resident: the pair's CTAs share what its length has
+    const int blocks = L < 1 || L > Lcap ? 0 : (L + bs - 1) >> lbs;
+    per = min(p.per, max((blocks + p.max_chunks - 1) / p.max_chunks, p.fit));
+    j0 = ((int)blockIdx.x - pair * p.max_chunks) * per;
+    j1 = min(p.k, j0 + per);
+  }
   const int64_t qh0 = (int64_t)b * p.Hq + (int64_t)h * g;
   // lane l's tiles l and l + 32 of this warp (steps warp, warp + W, .. of the
   // range, kStep tiles each): their block indices are requested before the
@@ -318,7 +325,6 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   if constexpr (kInt4) {
     if ((tid >> 4) < g) qw = __ldg(reinterpret_cast<const uint4*>(p.q + (qh0 + (tid >> 4)) * kHeadDim) + (tid & 15));
   }
-  const int L = __ldg(p.seq_lens + b);
   const bool bad_len = L < 1 || L > Lcap;
   const int nb = bad_len ? 0 : (L + bs - 1) >> lbs;
   int cnt = p.sel_idx ? __ldg(p.sel_cnt + pair) : nb;
@@ -339,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   if (ntiles <= 0) continue;
   // the pair's ranges that hold a kept block, and this one's place among them
   const int first_cta = pair * p.stride / p.per;
-  const int nchunks = (pair * p.stride + cnt - 1) / p.per - first_cta + 1, chunk = blockIdx.x - first_cta;
+  const int nchunks = p.fit ? (cnt + per - 1) / per : (pair * p.stride + cnt - 1) / p.per - first_cta + 1;
+  const int chunk = blockIdx.x - first_cta;
 
   // the warp's tiles' first rows (a cache of 2^31 rows is larger than the
   // memory); a tile of less than 16 rows is marked and their number kept aside

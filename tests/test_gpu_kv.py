@@ -319,7 +319,7 @@ def logit_delta(c, q, int4, scale, g):
     return float(each.max()) * scale + 2.0**-22 * 64
 
 
-def check_attention(c, q, out, lse, acc, acc0, int4, sel=None, scale=1 / math.sqrt(D)):
+def check_attention(c, q, out, lse, acc, acc0, int4, sel=None, scale=1 / math.sqrt(D), tiles=32):
     g = q.shape[1] // c.Hkv
     hk, hv = c.held() if int4 else (c.k.double().nan_to_num(0), c.v.double().nan_to_num(0))
     o, l, w, spread = ref.attend(q, hk, hv, [max(n, 0) for n in c.lens], sel, scale, c.bs)
@@ -330,7 +330,7 @@ def check_attention(c, q, out, lse, acc, acc0, int4, sel=None, scale=1 / math.sq
     tol = 2.0**-8 * o.abs() + (2.0**-10 if int4 else 2.0**-16) * spread + (2 * delta + 2.0**-19) * spread + 2.0**-140
     if int4:
         step = ref.quantise(c.v)[1].nan_to_num(0).repeat_interleave(32, -1)
-        tol += 2.0**-13 * ref.attend(q, hk, step, [max(n, 0) for n in c.lens], sel, scale, c.bs)[0]
+        tol += tiles / 32 * 2.0**-13 * ref.attend(q, hk, step, [max(n, 0) for n in c.lens], sel, scale, c.bs)[0]
     err = (out.double() - o).abs()
     assert (err <= tol).all(), float((err / tol).max())
     assert (out[~some] == 0).all()
@@ -819,3 +819,30 @@ def test_binding_refuses_short_and_foreign_tensors():
         call(q=q[:, :1])
     with pytest.raises(kin.KinError):
         kin.kin_kv4_load(d, c.bf16(), c.seq, c.k.clone(), c.v.clone())  # not a 4-bit cache
+
+
+@pytest.mark.parametrize("int4", [True, False], ids=["int4", "bf16"])
+@pytest.mark.parametrize("lens, Hkv, bs, cap", [
+    ([113_003], 2, 16, 113_100),          # few pairs, a range for every resident CTA
+    ([16_000, 1, 0, 4_097], 24, 16, 16_001),   # 96 pairs: ranges of 250 tiles, cut anew for the short ones
+    ([17, 7_000], 4, 64, 131_072),        # short sequences in a large cache
+], ids=["one_long", "long_ranges", "large_cache"])
+def test_long_dense_ranges(lens, Hkv, bs, cap, int4):
+    """Every token of sequences whose ranges hold up to 256 tiles, 64 a warp:
+    23 * 64 * 2^-23 < 2^-12 of sum p s, twice the bound above.  Sums: a thread
+    adds 2 weights a tile and head and 222 ranges at most are merged, each
+    addition to 2^-24: 350 * 2^-24 < 2^-15.5.  delta holds 2^-22 * 64 = 2^-16
+    for a scaling that takes 2^-19 (logits below 32); with 2^-20 (1 + |lse|),
+    lse > 9 where that many ranges meet, the lse has 2^-15.3 for it, and a
+    weight, with delta twice, 2^-15."""
+    c = Cache(lens, Hkv, bs, cap, False, 171)
+    g, st = 2, status()
+    q = rows16(172, c.B, Hkv * g, D)
+    d = c.dims(g)
+    kv = c.stored() if int4 else c.bf16()
+    out, lse = torch.full_like(q, 7.0), torch.full((c.B, Hkv * g), 7.0, device="cuda")
+    acc = torch.zeros((c.B, Hkv, cap), device="cuda")
+    ws = kin.alloc_kv_attn_workspace(d, 0, acc=True)
+    kin.kin_kv_decode_attn(d, q, kv, c.seq, None, None, 0, 0.0, out, lse, ws, acc=acc, dev_status=st)
+    assert int(st.item()) == (5 if 0 in lens else 0)
+    check_attention(c, q, out, lse, acc, None, int4, tiles=64)
