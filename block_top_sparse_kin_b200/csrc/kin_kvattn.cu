@@ -689,11 +689,18 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
                                      {hmul2(p0, va.z), hmul2(p1, vb.z)}, {hmul2(p0, va.w), hmul2(p1, vb.w)}};
           // value codes: the lane's 4 channels of each group, of its 4 tokens.
           // Two tokens' halfwords side by side; of a byte of each, the low
-          // nibbles (n 2^-24) for one channel, and both (n 2^-24 + n' 2^-20)
+          // nibbles (n 2^-18) for one channel, and both (n 2^-24 + n' 2^-20)
           // for the next, whose sum the first channel's comes off at the end.
           // So does 8 times the weights' sum, taken by a product with a row of
           // ones for each group (a warp's tiles are few enough for the
           // difference to keep its bits).
+          // The instruction lines its products up by the operands' exponents
+          // and keeps 25 bits below the largest (measured); a subnormal's is
+          // that of 2^-14, so where a code stands decides what is left of the
+          // light tokens beside a heavy one.  n 2^-18 keeps them down to 2^-21
+          // of its weight, n 2^-24 would to 2^-15: where the heavy code is 0 the
+          // output was then off by up to 2^-12 of a step.  32 x 8 pairs of 4096
+          // tokens take 0.8 us more for it.
           uint2 x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -708,8 +715,8 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
             const uint32_t l01 = u01 & 0x00FF00FFu, l23 = u23 & 0x00FF00FFu;
             const uint32_t h01 = __byte_perm(u01, 0u, 0x4341), h23 = __byte_perm(u23, 0u, 0x4341);
             const uint32_t one = tq == G ? 0x3C003C00u : 0u;
-            mma_f16_16816(a.o[2 * G], u01 & 0x000F000Fu, l01, u23 & 0x000F000Fu, l23, pb[G][0], pb[G][1]);
-            mma_f16_16816(a.o[2 * G + 1], h01 & 0x000F000Fu, h01, h23 & 0x000F000Fu, h23, pb[G][0], pb[G][1]);
+            mma_f16_16816(a.o[2 * G], (u01 << 6) & 0x03C003C0u, l01, (u23 << 6) & 0x03C003C0u, l23, pb[G][0], pb[G][1]);
+            mma_f16_16816(a.o[2 * G + 1], (h01 << 6) & 0x03C003C0u, h01, (h23 << 6) & 0x03C003C0u, h23, pb[G][0], pb[G][1]);
             mma_f16_16816(a.sums, one, 0u, one, 0u, pb[G][0], pb[G][1]);
           }
         }
@@ -766,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float off = -8.f * __shfl_sync(0xffffffffu, a.sums[j], G * 4 + c);
-          const float x0 = a.o[2 * G][j] * 0x1p24f, x2 = a.o[2 * G + 1][j] * 0x1p24f;
+          const float x0 = a.o[2 * G][j] * 0x1p18f, x2 = a.o[2 * G + 1][j] * 0x1p18f;
           const float x1 = fmaf(a.o[2 * G][2 + j], 0x1p20f, x0 * -0x1p-4f), x3 = fmaf(a.o[2 * G + 1][2 + j], 0x1p20f, x2 * -0x1p-4f);
           *reinterpret_cast<float4*>(w0 + j * kRowPad + 32 * G + 4 * tq) =
               make_float4((x0 + off) * vn, (x1 + off) * vn, (x2 + off) * vn, (x3 + off) * vn);
