@@ -184,12 +184,12 @@ __device__ __forceinline__ uint32_t tok_mask(int t, int nvalid) {
 // A head's weights are 2^(z - r) with a reference r that follows the running
 // maximum m of its logits loosely: r = m - lead, and m moves (all sums are
 // then rescaled) only when a logit passes m + kSlack.  So a tile usually
-// costs no reduction over its tokens.  4 bit: weights reach 2^14, in the
-// middle of fp16's range.  bf16: weights stay below 1, so that values of any
+// costs no reduction over its tokens.  4 bit: weights reach 2^15, near the top
+// of fp16's range.  bf16: weights stay below 1, so that values of any
 // magnitude add up.
 constexpr float kSlack = 8.f;
 template <bool kInt4>
-constexpr float kLead = kInt4 ? 6.f : -kSlack;
+constexpr float kLead = kInt4 ? 7.f : -kSlack;
 
 // The sums of a warp: O^T fragments, and for its two head columns the maximum
 // logit followed, before the scaling to base 2 (raw), the reference and the
@@ -511,9 +511,18 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   // 4 bit: the second product's weights p vs are fp16 (11 bits; a bf16 weight
   // would cost as much accuracy as the final rounding): p, and vs divided by
   // vn, a power of two above the group's largest scale in this warp so far (at
-  // least 2^-100).  Lane l keeps the vn of group l % 4.
+  // least 2^-100; lane l keeps the vn of group l % 4).  That holds while every
+  // scale is at least 2^-10 vn: vs / vn is then exact, the heaviest token has p
+  // >= 2^7, so the weights' sum is at least 2^-3 vn, and what fp16's least step
+  // takes from the small weights of a warp's 1024 tokens, at most 2 * 2^-25 vn
+  // each, is 2^-11 of it.  From the first step with a smaller scale on (a row
+  // of zeros has none) the warp forms its weights in fp32 and each step has
+  // factors of its own (below).  least: a bound below the scales of the
+  // lane's tokens, looked after when a step leaves [2^-8 vn, vn).
+  constexpr float kFlat = 0x1p-8f, kWide = 0x1p-10f;
+  constexpr uint32_t kFlat16 = 0x1C001C00u;  // kFlat in fp16; 0x2000 above it is 1
   uint32_t vn_bits = 27u << 23;
-  float inv_vn = 0x1p100f;
+  float least = __int_as_float(0x7f800000);
   bool v_nan = false;
   uint32_t slot = 0;
 
@@ -544,24 +553,28 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
         // scales of a token pair of the second product's slots
         const int tp = (tq & 3) + 8 * (tq >> 2), tp2 = tp ^ 5;  // ((tp & 3) ^ 1) + 4
         float v[kStep][2];
-        const float vn = __uint_as_float(vn_bits);
-        bool high = false;
+        uint32_t vx[kStep], off = 0u;
 #pragma unroll
         for (int h = 0; h < kStep; ++h) {
           const uint32_t kw = lds32(base + h * R::kTileBytes + 2048 + lane * 4);
           v[h][0] = __uint_as_float(lds16(base + h * R::kTileBytes + 2176 + tp * 8 + c * 2) << 16);
           v[h][1] = __uint_as_float(lds16(base + h * R::kTileBytes + 2176 + tp2 * 8 + c * 2) << 16);
           sts64(scales + h * R::kScaleBytes + lane * 8, lo_f(kw), hi_f(kw));
-          high |= !(v[h][0] < vn) || !(v[h][1] < vn);
+          const float inv_vn = __uint_as_float((254u << 23) - vn_bits);
+          vx[h] = pack_f16x2(v[h][0] * inv_vn, v[h][1] * inv_vn);
+          off |= vx[h] - kFlat16;  // NaN too is behind 1; a borrow comes only from a half that is off
         }
-        if (__any_sync(0xffffffffu, high)) {
+        if (__any_sync(0xffffffffu, (off & 0xE000E000u) != 0u)) {
           // a scale that is not finite makes its group NaN whatever its
           // weight: noted here, and kept out of the products
+          const float vn = __uint_as_float(vn_bits);
           uint32_t mb = 0u;
+          if (st > 0) least = fminf(least, vn * kFlat);  // the steps that did not come here
 #pragma unroll
           for (int h = 0; h < kStep; ++h) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+              if ((i ? tp2 : tp) < nv[h]) least = fminf(least, v[h][i]);
               if (!(v[h][i] < 0x1p127f)) {
                 v_nan = true;
                 v[h][i] = 0.f;
@@ -569,12 +582,11 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
               if (v[h][i] > 0.f) mb = max(mb, __float_as_uint(v[h][i]));
             }
           }
-          // a larger one moves the group's sums to its power of two
+          // a larger one moves the group's sums to a power of two with some room above it
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, off));
-          const uint32_t e = mb >= vn_bits ? min((mb >> 23) + 1u, 253u) : vn_bits >> 23;
-          inv_vn = __uint_as_float((254u - e) << 23);
-          const float down = vn * inv_vn;
+          const uint32_t e = mb >= vn_bits ? min((mb >> 23) + 3u, 253u) : vn_bits >> 23;
+          const float down = vn * __uint_as_float((254u - e) << 23);
           vn_bits = e << 23;
           const float mine = __shfl_sync(0xffffffffu, down, tq & 3);
 #pragma unroll
@@ -585,10 +597,14 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
 #pragma unroll
             for (int i = 0; i < 4; ++i) a.o[dm][i] *= dg;
           }
+#pragma unroll
+          for (int h = 0; h < kStep; ++h) {
+            const float inv_vn = __uint_as_float((254u << 23) - vn_bits);
+            vx[h] = pack_f16x2(v[h][0] * inv_vn, v[h][1] * inv_vn);
+          }
         }
 #pragma unroll
-        for (int h = 0; h < kStep; ++h)
-          sts32(scales + h * R::kScaleBytes + 256 + lane * 4, pack_f16x2(v[h][0] * inv_vn, v[h][1] * inv_vn));
+        for (int h = 0; h < kStep; ++h) sts32(scales + h * R::kScaleBytes + 256 + lane * 4, vx[h]);
         __syncwarp();
         uint4 wa[kStep], wb[kStep], sa[kStep], sb[kStep];
 #pragma unroll
@@ -678,7 +694,69 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
         }
       }
       weigh<kInt4>(a, s, sl2, pr);
-      if constexpr (kInt4) {
+      // (least falls and vn grows, so a warp stays on this way; a vote a step costs less than a flag kept)
+      if (kInt4 && __any_sync(0xffffffffu, least < __uint_as_float(vn_bits) * kWide)) {
+        // Scales far apart, so a token that weighs nothing must not set the
+        // others' factor, nor one head's tokens another's: the products p vs /
+        // vn in fp32, and per head and group of this step a power of two that
+        // takes the largest of them to [2^14, 2^15) before they become fp16.
+        // The step's sums start from zero, every code as n 2^-18, and join the
+        // running ones in fp32, whose range ends 2^80 below vn.
+        // 32 x 8 pairs of 4096 tokens, 64 tokens apart a scale of 10^-4: 58.5 us
+        // where every step is of this kind, 42.5 without.
+#pragma unroll
+        for (int G = 0; G < 4; ++G) {
+          const float inv = __shfl_sync(0xffffffffu, __uint_as_float((254u << 23) - vn_bits), G);
+          float w[kStep][4], top[2] = {0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < kStep; ++h) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float vs = __uint_as_float(lds16(base + h * R::kTileBytes + 2176 + (i < 2 ? t0 : t1) * 8 + G * 2) << 16);
+              w[h][i] = pr[h][i] * (vs < 0x1p127f ? vs * inv : 0.f);  // not finite: noted above
+              top[i & 1] = fmaxf(top[i & 1], w[h][i]);
+            }
+          }
+          float up[2], down[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], off));
+            const uint32_t e = max(__float_as_uint(top[j]) >> 23, 15u);  // biased exponent; 255 (not finite) at most
+            up[j] = __uint_as_float((268u - e) << 23);
+            down[j] = __uint_as_float((e - 14u) << 23);
+          }
+          float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f}, ds[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < kStep; ++h) {
+            const uint32_t p0 = movmatrix_trans(pack_f16x2(w[h][0] * up[0], w[h][1] * up[1]));
+            const uint32_t p1 = movmatrix_trans(pack_f16x2(w[h][2] * up[0], w[h][3] * up[1]));
+            const uint32_t sel = (G & 1) ? 0x7632u : 0x5410u;
+            uint32_t x[4];  // value codes, as below
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int t = 4 * i + ((i & 1) ? c ^ 1 : c);
+              x[i] = lds32(base + h * R::kTileBytes + 1024 + t * 64 + (((tq >> 1) ^ (t & 2)) << 4) + (tq & 1) * 8 + (G >> 1) * 4);
+            }
+            const uint32_t u01 = __byte_perm(x[0], x[1], sel), u23 = __byte_perm(x[2], x[3], sel);
+            const uint32_t one = tq == G ? 0x3C003C00u : 0u;
+            mma_f16_16816(d0, (u01 << 6) & 0x03C003C0u, (u01 << 2) & 0x03C003C0u, (u23 << 6) & 0x03C003C0u,
+                          (u23 << 2) & 0x03C003C0u, p0, p1);
+            mma_f16_16816(d1, (u01 >> 2) & 0x03C003C0u, (u01 >> 6) & 0x03C003C0u, (u23 >> 2) & 0x03C003C0u,
+                          (u23 >> 6) & 0x03C003C0u, p0, p1);
+            mma_f16_16816(ds, one, 0u, one, 0u, p0, p1);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float f = down[j] * 0x1p-6f;
+            a.o[2 * G][j] = fmaf(d0[j], down[j], a.o[2 * G][j]);
+            a.o[2 * G][2 + j] = fmaf(fmaf(d0[2 + j], 16.f, d0[j]), f, a.o[2 * G][2 + j]);
+            a.o[2 * G + 1][j] = fmaf(d1[j], down[j], a.o[2 * G + 1][j]);
+            a.o[2 * G + 1][2 + j] = fmaf(fmaf(d1[2 + j], 16.f, d1[j]), f, a.o[2 * G + 1][2 + j]);
+            a.sums[j] = fmaf(ds[j], down[j], a.sums[j]);
+          }
+        }
+      } else if constexpr (kInt4) {
 #pragma unroll
         for (int h = 0; h < kStep; ++h) {
           const uint32_t tb = base + h * R::kTileBytes, sc = scales + h * R::kScaleBytes + 256;

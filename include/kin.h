@@ -399,10 +399,13 @@ kin_status kin_kv4_load(const kin_dims* dims, const kin_kv* kv, const int32_t* s
  * summed over the group's query heads:
  *   acc[b][h][t] += sum_{j of h} e^{z_jt - lse_j}.
  * A block listed twice is attended to, and weighed, twice.  Weights are
- * rounded to 11 (4 bit) or 16 (bf16) bits before they meet the values; sums
- * are fp32.  NaN logits or values give NaN outputs.  Over 4-bit rows, queries
- * below 2^118 and values below 2^96 in magnitude are safe from overflow.  A length outside
- * [1, Lcap] gets out = 0, lse = -inf and flags KIN_ERR_DEVICE_DATA.
+ * rounded to 11 (4 bit) or 16 (bf16) bits before they meet the values; over
+ * 4-bit rows the smallest ones lose at most 2^-11 of sum p s in all (s a
+ * token's scale), however far the tokens' weights are apart, and their scales
+ * up to 2^80.  Sums are fp32.  NaN logits or values give NaN outputs.  Over
+ * 4-bit rows, queries below 2^118 and values below 2^96 in magnitude are safe
+ * from overflow.  A length outside [1, Lcap] gets out = 0, lse = -inf and
+ * flags KIN_ERR_DEVICE_DATA.
  * workspace: kin_kv_attn_workspace_bytes for the same k_blocks (with_acc 1
  * where acc is given), 256-byte aligned and zero-filled before its first use
  * like kin_workspace_bytes'; with k_blocks >= 2 it serves the select calls

@@ -1,5 +1,5 @@
-"""Attention over 4-bit caches where some tokens weigh far more than others.
-Plain forms, caches and tolerances are test_gpu_kv's; what they have to hold
+"""Attention over 4-bit caches where some tokens weigh far more than others, or
+have far larger values.  Plain forms, caches and tolerances are test_gpu_kv's; what they have to hold
 here besides:
 
 A tile's product keeps 25 bits below the largest of its exponents' sums, and a
@@ -9,6 +9,11 @@ the tile's largest weight, 2^-21 or 2^-19 after the scaling back, 16 of them
 2^-15, and the tiles' largest weights add up to no more than sum p.  The
 running sums take 9 tiles' additions, 23 * 9 * 2^-23 < 2^-15 of sum p s.  Both
 stay below the 2^-13 of sum p s that check_attention allows.
+
+Scales: where a warp's all lie within 2^10 of its largest vn, fp16 takes at
+most 2 * 2^-25 vn from a small weight, and sum p s >= 2^-3 vn (in units where
+the heaviest token has 2^7): 130 tokens * 2^-24 * 2^3 = 2^-14 of it.
+Elsewhere a step's largest weight is 2^14 or more in fp16: 32 * 2^-25 * 2^-14.
 """
 import pytest
 import torch
@@ -48,3 +53,56 @@ def test_heavy_tokens_leave_the_light_ones_their_bits(at, where):
     c = Cache([300], 2, 16, 300, False, 211)
     q = pointed(c, PLACES[where], at=at)
     check_attention(c, q, *attended(c, q), None, True)
+
+
+@pytest.mark.parametrize("where", PLACES)
+@pytest.mark.parametrize("power", [7, 9, 11, 12, 18, 22, 26, 60, 78])
+def test_huge_values_under_tiny_weights(power, where):
+    """Tokens with huge values that weigh next to nothing leave the others'
+    bits alone, and reach the output with what they do weigh: 2^-65, 2^-49 and
+    2^-33 of the heaviest for three heads; the fourth reads them alone."""
+    c = Cache([300], 2, 16, 300, False, 201)
+    q = pointed(c, PLACES[where])
+    c.v[:, :, PLACES[where]] *= 2.0**power
+    check_attention(c, q, *attended(c, q), None, True)
+
+
+@pytest.mark.parametrize("where", PLACES)
+@pytest.mark.parametrize("power", [None, -78, -60, -30, -20, -12, -9])
+def test_the_heaviest_tokens_have_small_values(power, where):
+    """The tokens that take the whole softmax have no value, or a tiny one; the output is the others'."""
+    c = Cache([300], 2, 16, 300, False, 211)
+    q = pointed(c, PLACES[where], at=4.0)
+    c.v[:, :, PLACES[where]] *= 0.0 if power is None else 2.0**power
+    check_attention(c, q, *attended(c, q), None, True)
+
+
+def test_values_grow_and_shrink_under_sharp_weights():
+    """Every token's scale another power of two, over 2^70, rising, falling
+    and mixed, with weights that rise and fall as steeply."""
+    c = Cache([480, 480, 480], 2, 16, 480, True, 221)
+    q = pointed(c, [], at=0.0)
+    steep = torch.linspace(-35, 35, 480, device="cuda")
+    mixed = steep[torch.randperm(480, generator=gen(222), device="cuda")]
+    u = q[0, 0].float()
+    for b, p in enumerate((steep, steep.flip(0), mixed)):
+        c.v[b] = (c.v[b].float() * 2.0 ** p[:, None]).to(torch.bfloat16)
+        # logits of the first head: -ln 2 of the scale's power, so every token weighs in alike
+        c.k[b] = (c.k[b].float() * 0.2 - p[:, None] * (0.6931 * 11.3137 / 128) * u).to(torch.bfloat16)
+    check_attention(c, q, *attended(c, q), None, True)
+
+
+def test_a_not_finite_group_beside_wide_scales():
+    """NaN and infinite values among scales far apart: their 32 channels alone are NaN."""
+    c = Cache([300], 2, 16, 300, False, 231)
+    q = pointed(c, [50])
+    c.v[:, :, 50] *= 2.0**30
+    c.v[0, 0, 20, 5], c.v[0, 0, 200, 70] = float("nan"), float("inf")
+    out, lse, acc = attended(c, q)
+    gone = torch.zeros((1, 8, D), dtype=torch.bool, device="cuda")
+    gone[0, :4, :32], gone[0, :4, 64:96] = True, True
+    assert torch.equal(out.isnan(), gone)
+    c.v[0, 0, 20, :32], c.v[0, 0, 200, 64:96] = 0, 0  # the other groups are as without them
+    out2, lse2, acc2 = attended(c, q)
+    check_attention(c, q, out2, lse2, acc2, None, True)
+    assert torch.equal(lse, lse2) and torch.equal(acc, acc2)
