@@ -185,11 +185,13 @@ __device__ __forceinline__ uint32_t tok_mask(int t, int nvalid) {
 // maximum m of its logits loosely: r = m - lead, and m moves (all sums are
 // then rescaled) only when a logit passes m + kSlack.  So a tile usually
 // costs no reduction over its tokens.  4 bit: weights reach 2^15, near the top
-// of fp16's range.  bf16: weights stay below 1, so that values of any
-// magnitude add up.
+// of fp16's range.  bf16: weights stay below 2^-22 and a pair attends to at
+// most 2^22 tokens (32768 blocks of 128), so no sum of weights passes 1, in a
+// warp or over the ranges, and values of any magnitude average without
+// overflow; from 2^-80 down they come near the end of fp32.
 constexpr float kSlack = 8.f;
 template <bool kInt4>
-constexpr float kLead = kInt4 ? 7.f : -kSlack;
+constexpr float kLead = kInt4 ? 7.f : -kSlack - 22.f;
 
 // The sums of a warp: O^T fragments, and for its two head columns the maximum
 // logit followed, before the scaling to base 2 (raw), the reference and the
@@ -876,7 +878,8 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   }
   __syncthreads();
   auto write_lse = [&](int j, float den, float M) {
-    const float l2 = den == 0.f ? kNegInf : M + log2f(den);
+    // in the sum's own units: M + lead is the reference logit
+    const float l2 = den == 0.f ? kNegInf : (M + kLead<kInt4>) + log2f(den * (kInt4 ? 0x1p-7f : 0x1p30f));
     if (p.lse) p.lse[qh0 + j] = l2 * 0.6931471805599453f;
     if (kAcc) p.lse2[qh0 + j] = l2;
     s_inv[j] = den == 0.f ? 0.f : __frcp_rn(den);

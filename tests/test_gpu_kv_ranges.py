@@ -1,6 +1,6 @@
-"""Attention over 4-bit caches where some tokens weigh far more than others, or
-have far larger values.  Plain forms, caches and tolerances are test_gpu_kv's; what they have to hold
-here besides:
+"""Attention over caches where some tokens weigh far more than others, or have
+far larger values.  Plain forms, caches and tolerances are test_gpu_kv's; what
+they have to hold here besides:
 
 A tile's product keeps 25 bits below the largest of its exponents' sums, and a
 code enters as n 2^-18 (even channels) or, of a byte, as n 2^-24 + n' 2^-20
@@ -14,6 +14,9 @@ Scales: where a warp's all lie within 2^10 of its largest vn, fp16 takes at
 most 2 * 2^-25 vn from a small weight, and sum p s >= 2^-3 vn (in units where
 the heaviest token has 2^7): 130 tokens * 2^-24 * 2^3 = 2^-14 of it.
 Elsewhere a step's largest weight is 2^14 or more in fp16: 32 * 2^-25 * 2^-14.
+
+bf16: a logit's distance from the reference is at most 64 here, so a weight's
+exponent is rounded by 2^-19 at most, within the 2^-19 of check_attention.
 """
 import pytest
 import torch
@@ -106,3 +109,19 @@ def test_a_not_finite_group_beside_wide_scales():
     out2, lse2, acc2 = attended(c, q)
     check_attention(c, q, out2, lse2, acc2, None, True)
     assert torch.equal(lse, lse2) and torch.equal(acc, acc2)
+
+
+@pytest.mark.parametrize("n,bs", [(4096, 16), (20000, 128)])
+def test_bf16_values_at_the_ends_of_their_range(n, bs):
+    """Thousands of equal weights on the largest values of one sign average to
+    that value; values near 2^-76 keep their bits."""
+    c = Cache([n], 1, bs, n, False, 241)
+    d = c.dims(8)
+    ws = kin.alloc_kv_attn_workspace(d, 0)
+    for v, q in ((torch.full_like(c.v, 3.3e38), torch.zeros((1, 8, D), dtype=torch.bfloat16, device="cuda")),
+                 (torch.full_like(c.v, -3.3e38), rows16(242, 1, 8, D)),
+                 ((c.v.float() * 2.0**-76).to(torch.bfloat16), rows16(243, 1, 8, D))):
+        c.v = v
+        out, lse = torch.full_like(q, 9.0), torch.empty((1, 8), device="cuda")
+        kin.kin_kv_decode_attn(d, q, c.bf16(), c.seq, None, None, 0, 0.0, out, lse, ws)
+        check_attention(c, q, out, lse, None, None, False)
