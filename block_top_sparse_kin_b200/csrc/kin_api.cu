@@ -653,6 +653,28 @@ kin_status means_layout(const kin_dims& d, const KvView& kv, const void* means, 
 // The two share a buffer, a page pool included.
 bool same_cache(const KvView& a, const KvView& b) { return a.k == b.k || a.v == b.v || a.k == b.v || a.v == b.k; }
 
+// n bytes at a and m bytes at b share one.
+bool meet(const void* a, size_t n, const void* b, size_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + m && y < x + n;
+}
+
+size_t kv_rows(const kin_dims& d, const KvView& v) {
+  return v.pages.table ? (size_t)v.pages.num_pages * d.num_kv_heads * d.block_size : (size_t)pairs_of(d) * d.max_seq_len;
+}
+
+// n bytes at a and the cache's rows or scales share one.
+bool meets_cache(const void* a, size_t n, const kin_dims& d, const KvView& v) {
+  const size_t rows = kv_rows(d, v), codes = rows * (v.int4 ? kCodeBytes : kHeadDim * 2), scales = rows * kGroups * 2;
+  return meet(a, n, v.k, codes) || meet(a, n, v.v, codes) || meet(a, n, v.ks, scales) || meet(a, n, v.vs, scales);
+}
+
+bool caches_meet(const kin_dims& da, const KvView& a, const kin_dims& db, const KvView& b) {
+  const size_t rows = kv_rows(da, a), codes = rows * (a.int4 ? kCodeBytes : kHeadDim * 2), scales = rows * kGroups * 2;
+  return meets_cache(a.k, codes, db, b) || meets_cache(a.v, codes, db, b) || meets_cache(a.ks, scales, db, b) ||
+         meets_cache(a.vs, scales, db, b);
+}
+
 // How the attention cuts the (pair, kept block) slots into ranges of `per`
 // blocks, one per CTA.  A pair's slots are padded to `stride`: a multiple of
 // per (aligned: no range crosses a pair), or k itself (ranges that run on into
@@ -764,6 +786,7 @@ KIN_EXPORT kin_status kin_kv4_store(const kin_dims* dims, const kin_kv* src, con
   KvView s, d;
   if ((st = kv_view(*dims, src, &s)) != KIN_OK || (st = kv_view(*dims, dst, &d)) != KIN_OK) return st;
   if (s.int4 || !d.int4 || !seq_lens) return KIN_ERR_INVALID_ARG;
+  if (caches_meet(*dims, s, *dims, d)) return KIN_ERR_INVALID_ARG;  // rows are read in no order
   Kv4WriteParams p{};
   st = means_layout(*dims, d, block_means, means_dtype, &p.means_flag, &p.means_per_page, &p.mean_rows);
   if (st != KIN_OK) return st;
@@ -793,6 +816,8 @@ KIN_EXPORT kin_status kin_kv4_append(const kin_dims* dims, const kin_kv* kv, voi
   if ((st = kv_view(*dims, kv, &d)) != KIN_OK) return st;
   if (!d.int4 || !seq_lens || !new_lens || !k_new || !v_new) return KIN_ERR_INVALID_ARG;
   if (!aligned16(k_new) || !aligned16(v_new)) return KIN_ERR_INVALID_ARG;
+  const size_t lens_bytes = (size_t)dims->batch * sizeof(int32_t);
+  if (new_lens != seq_lens && meet(new_lens, lens_bytes, seq_lens, lens_bytes)) return KIN_ERR_INVALID_ARG;
   Kv4WriteParams p{};
   st = means_layout(*dims, d, block_means, means_dtype, &p.means_flag, &p.means_per_page, &p.mean_rows);
   if (st != KIN_OK) return st;
@@ -827,6 +852,10 @@ KIN_EXPORT kin_status kin_kv4_load(const kin_dims* dims, const kin_kv* kv, const
   if ((st = kv_view(*dims, kv, &s)) != KIN_OK) return st;
   if (!s.int4 || !seq_lens || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return KIN_ERR_INVALID_ARG;
   if (n == 0) return KIN_OK;
+  const size_t out_bytes = (size_t)pairs_of(*dims) * n * kHeadDim * 2;
+  if (meet(k_out, out_bytes, v_out, out_bytes) || meets_cache(k_out, out_bytes, *dims, s) ||
+      meets_cache(v_out, out_bytes, *dims, s))
+    return KIN_ERR_INVALID_ARG;
   Kv4LoadParams p{};
   p.src = s;
   p.seq_lens = seq_lens;
@@ -943,7 +972,11 @@ KIN_EXPORT kin_status kin_kv_evict(const kin_dims* dims, const kin_kv* kv, const
   if (same_cache(p.src, p.dst) && !(p.src.pages.table && p.dst.pages.table && p.src.k == p.dst.k && p.src.v == p.dst.v))
     return KIN_ERR_INVALID_ARG;
   if (p.src.pages.table && p.src.pages.table == p.dst.pages.table && p.src.k == p.dst.k) return KIN_ERR_INVALID_ARG;
-  if (dst_acc == acc || dst_lens == seq_lens) return KIN_ERR_INVALID_ARG;
+  if (!(p.src.pages.table && p.dst.pages.table) && caches_meet(*dims, p.src, *dst_dims, p.dst)) return KIN_ERR_INVALID_ARG;
+  const size_t acc_bytes = (size_t)pairs_of(*dims) * sizeof(float), lens_bytes = (size_t)dims->batch * sizeof(int32_t);
+  if (meet(acc, acc_bytes * dims->max_seq_len, dst_acc, acc_bytes * dst_dims->max_seq_len) ||
+      meet(seq_lens, lens_bytes, dst_lens, lens_bytes))
+    return KIN_ERR_INVALID_ARG;
   st = means_layout(*dst_dims, p.dst, block_means, means_dtype, &p.means_flag, &p.means_per_page, &p.mean_rows);
   if (st != KIN_OK) return st;
   const EvictWs w = evict_ws_layout(*dims, n_keep);

@@ -370,7 +370,8 @@ typedef struct {
  * in the 4-bit cache dst (the two may have different block tables), and the
  * means of their blocks.  Rows and blocks behind the length are left as they
  * were.  A length outside [0, Lcap], or a page index outside its pool, skips
- * that sequence or block and flags KIN_ERR_DEVICE_DATA. */
+ * that sequence or block and flags KIN_ERR_DEVICE_DATA.  The two caches share
+ * no memory (KIN_ERR_INVALID_ARG). */
 kin_status kin_kv4_store(const kin_dims* dims, const kin_kv* src, const kin_kv* dst, const int32_t* seq_lens,
                          void* block_means, int32_t means_dtype, int32_t* dev_status, void* stream);
 
@@ -378,7 +379,7 @@ kin_status kin_kv4_store(const kin_dims* dims, const kin_kv* src, const kin_kv* 
  * ([B][Hkv][n_new][D] bf16) go to rows seq_lens[b] + r, the means of the
  * blocks that hold one of them are taken again from all their rows, and
  * new_lens[b] = seq_lens[b] + n_new.  new_lens may be seq_lens itself (in
- * place; a second small launch then).  A length below 0 or with no room for
+ * place; a second small launch then), but not overlap it in part.  A length below 0 or with no room for
  * n_new is skipped, keeps its length and flags KIN_ERR_DEVICE_DATA.  An
  * append and a store of the same tokens leave the same bytes. */
 kin_status kin_kv4_append(const kin_dims* dims, const kin_kv* kv, void* block_means, int32_t means_dtype,
@@ -388,7 +389,8 @@ kin_status kin_kv4_append(const kin_dims* dims, const kin_kv* kv, void* block_me
 /* Reads rows starts[b] .. starts[b] + n - 1 of a 4-bit cache back as bf16
  * (each value rounded to nearest even) into k_out / v_out [B][Hkv][n][D].
  * starts NULL begins at 0; rows at or behind seq_lens[b] come back as zeros,
- * so do those of a bad length, start or page (flagged). */
+ * so do those of a bad length, start or page (flagged).  k_out, v_out and the
+ * cache share no memory (KIN_ERR_INVALID_ARG). */
 kin_status kin_kv4_load(const kin_dims* dims, const kin_kv* kv, const int32_t* seq_lens, const int32_t* starts,
                         int32_t n, void* k_out, void* v_out, int32_t* dev_status, void* stream);
 
@@ -425,7 +427,8 @@ kin_status kin_kv_decode_attn(const kin_dims* dims, const void* q, const kin_kv*
  * are no more.  Their rows move, in order, to rows 0, 1, ... of dst, a cache
  * of the same format with its own dims (all but max_seq_len equal) and its
  * own memory (another buffer, or pages of the same pool that no sequence
- * still reads: a page in both block tables is undefined).  dst_lens[b] =
+ * still reads: a page in both block tables is undefined; other memory shared
+ * by the two, by acc and dst_acc or by the lengths is KIN_ERR_INVALID_ARG).  dst_lens[b] =
  * min(seq_lens[b], n_keep); dst_acc ([B][Hkv][dst Lcap], may be NULL) takes
  * the kept weights and zeros behind them; sel_tokens ([B][Hkv][n_keep], may
  * be NULL) the kept tokens' old indices, ascending, -1 padded; block_means
