@@ -150,6 +150,7 @@ def load_library(path: str = LIB_PATH):
 
 # a CUDA tensor at hand means that CUDA is initialised: the raw queries are enough
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # where torch has none, by its public call
 
 
 def _dev(t: Optional[torch.Tensor], name: str, dtype=None, nullable=False, count: Optional[int] = None):
@@ -230,7 +231,9 @@ def _status(dev_status):
 
 def _stream(stream):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(_current_device())
+        if _current_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _current_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
