@@ -684,13 +684,15 @@ bool caches_meet(const kin_dims& da, const KvView& a, const kin_dims& db, const 
 // that short sequences leave few partials; not swept) to per blocks.  8 pairs, 8 heads,
 // a cache of 128K tokens that holds 8K: 17.1 us, 31.9 with the capacity's
 // ranges; 128 pairs, 2000 of 8192 tokens: 17.6 for 28.8; calls of a few short
-// sequences take 0.2 us more.
+// sequences take 0.2 us more.  (These and the times below were taken with a
+// build whose 4-bit tiles took 2 to 4% less than now, on either side alike.)
 struct KvSplit {
   int per, stride, fit;
 };
 
-// Chosen by an estimate in microseconds, from timings of 4-bit caches (bf16
-// tiles take two and a half times as long, which leaves the order as it is):
+// Chosen by an estimate in microseconds, from timings of 4-bit caches; bf16
+// tiles take two and a half times as long and are cut alike (16 x 8 pairs of
+// 8192 such tokens: 84.0 us, 83.5 in shorter ranges):
 // a range takes 4, or 5 where ranges of a pair are merged, and a tile 0.109,
 // 0.149 or 0.216 with one, two or three CTAs on an SM.  256 pairs of 256
 // tiles: 42.5 with one range each, 52.9 with two, 41.8 with even ranges over
@@ -724,7 +726,7 @@ KvSplit kv_split(const kin_dims& d, int k, bool dense) {
   }
   // dense: longer ranges where one wave holds them all, none waits for another
   // (8 pairs of 128K tokens, 8 heads: 50 us, 72 in ranges of 128 tiles or less;
-  // 128 pairs of 8192: 42 for 46.5; the same of bf16 rows, 4 heads: 84 for 83.5)
+  // 128 pairs of 8192: 42 for 46.5)
   if (dense && pairs <= wave) {
     const int c = (int)(wave / pairs), per = (k + c - 1) / c;
     if (per > most && per <= kKvItemTiles / tpb) consider(per);

@@ -351,7 +351,7 @@ __device__ __forceinline__ int64_t kv_row(const PageTable& pt, int b, int h, int
   return ((int64_t)page * Hkv + h) * bs + (t - i * bs);
 }
 
-// Store (first = 0, rows from a bf16 cache) and append (rows from k_new /
+// Store (append = 0, rows from a bf16 cache) and append (rows from k_new /
 // v_new behind the first seq_lens[b] tokens) into a 4-bit cache.
 struct Kv4WriteParams {
   KvView dst;

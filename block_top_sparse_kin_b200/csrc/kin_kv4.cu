@@ -19,10 +19,12 @@
 // 16-byte load of bf16), so a group is 4 lanes and its maximum two shuffles.
 // A warp has keys or values, never both (their orders would cost it both
 // paths), and to store, two consecutive blocks, one each half: a lane adds up
-// its 8 channels of a block's mean on the way.  All are streams bounded by
-// HBM; what they spend per row decides how near they come: 1M tokens stored
-// in 150 us (4.7 TB/s), read back in 108 us (6.4 TB/s); 512K bf16 tokens moved
-// in 87 us (6.0 TB/s).
+// its 8 channels of a block's mean on the way.  Reading back and the bf16 move
+// are streams bounded by HBM: 1M tokens read back in 108 us (6.4 TB/s), 512K
+// bf16 tokens moved in 87 us (6.0 TB/s).  The store is bounded by its
+// instructions, 122 a token: 1M tokens in 150 us (4.7 TB/s), where its bytes
+// would take 110.  Short stores and appends are bounded by their round trips
+// to memory, 4 rows of a block at a time (333 tokens to 32 pairs: 15 us).
 #include "kin_internal.cuh"
 
 namespace kin {
@@ -76,13 +78,13 @@ __device__ __noinline__ Codes8 encode8_tiny(uint4 w, float sf) {
 // the scale's bits (the same in the group's 4 lanes) and the codes c[i] as
 // numbers.
 //
-// The rounding is exact with one reciprocal.  x has an 8-bit significand S
-// and a midpoint (c + 1/2) s a product of an odd number 2c + 1 <= 13 and an
-// 8-bit one, so a quotient x / s that is not a midpoint is at least 2^-11
-// away from one (2^-8 of 1/2, 2^-10 of 3/2, 2^-11 of 5/2 and 7/2, 2^-12 of
-// 9/2 to 13/2).  x times the rounded reciprocal, added to 1.5 * 2^11 in one
-// rounding, is the quotient to 2^-13 + 2^-21 on a grid of 2^-12: at a midpoint
-// exactly there, elsewhere on its side of it.  The second addition rounds
+// The rounding is exact with one reciprocal.  x and s have significands X, S <
+// 2^8, and a midpoint is m / 2, m odd, so a quotient x / s = 2^n X / S that is
+// not a midpoint is at least 2^-9 away from it: by a whole number over 2 S, or
+// over 2^-n S, which is at most 2 X near a midpoint, where n < -1.  x times
+// the rounded reciprocal, added to 1.5 * 2^11 in one rounding, is the quotient
+// to 2^-13 + 2^-20 on a grid of 2^-12: at a midpoint exactly there, elsewhere
+// on its side of it.  The second addition rounds
 // that to a whole number, half to even, and the third leaves it.  A normal
 // scale is a / 7 to 2^-9, so no quotient reaches 7.5.  The scale itself: a / 7
 // is never a midpoint of bf16 (7 times an odd 9-bit number has 11 bits, a has

@@ -18,13 +18,15 @@
 // copies, 3 CTAs of 4 warps on an SM.  The bytes, 144 (4 bit) or 512 (bf16) a
 // token and pair, bound bf16 rows: 32 x 8 pairs, 4096 of 32768 tokens each, 4
 // heads: 87 us, 6.2 TB/s.  4-bit rows are bounded by what a tile costs the
-// SM: the same batch 41 us, 3.7 TB/s; 249 instructions a tile by
-// one warp, 102 of them for the logic unit (64 unpack its 4096 codes), no unit
-// over half busy, so warps wait on one another's bursts.  Measured on the
-// way there: nibbles through one conversion for two, 66 us; as fp16
+// SM: the same batch 41.7 us, 3.6 TB/s; 261 instructions a tile by one warp,
+// 102 of them for the logic unit (64 unpack its 4096 codes) and 84 multiply-
+// adds.  No unit is over half busy and half of the issue slots are empty: 12
+// warps an SM, each one dependent chain from the copies to the sums.  Measured
+// on the way there: nibbles through one conversion for two, 66 us; as fp16
 // subnormals, with no conversion, 49; two tiles a step, which share the
-// maximum, the copies' waits and the query loads, and even ranges, 42.  16
-// warps of 128 registers, one tile a step: 45.
+// maximum, the copies' waits and the query loads, and even ranges, 41; codes
+// placed so that light tokens keep their bits and scales watched, 41.7.  16
+// warps of 128 registers, one tile a step: 45 for 42.
 #include <type_traits>
 
 #include "kin_internal.cuh"
@@ -60,10 +62,11 @@ struct Ring {
 };
 
 // Rows are read once: their lines leave L2 before the logits and partials do.
-// 32 x 8 pairs of 4096 tokens, against copies without the hint: bf16 rows 86.4
-// us for 89.5, 4-bit rows 40.7 for 41.9; with weights 52.5 for 53.4 (4 bit) and
-// 102.5 for 103.1 (bf16), three caches in turn.  Called on one cache again and
-// again, bf16 with weights takes 95 for 103.
+// 32 x 8 pairs of 4096 tokens, against copies without the hint: bf16 rows 86.9
+// us for 89.2, 4-bit rows 42.2 for 43.9; with weights 53.6 for 55.0 (4 bit) and
+// 102.7 for 103.3 (bf16), three caches in turn (one build, 1% slower than the
+// last).  Called on one cache again and again, bf16 with weights takes 95 for
+// 103.
 __device__ __forceinline__ uint64_t read_once_policy() {
   uint64_t p;
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -458,10 +461,13 @@ __global__ void __launch_bounds__(kThreads, kKvCtasPerSm) kv_attn_kernel(KvAttnP
   // Queries.  4 bit: key nibbles enter the first product as the fp16 numbers
   // n 2^-24 (bits 0..3 of a half) and n 2^-20 (bits 4..7): one AND for two, no
   // conversion.  So q is fp16 too, each head scaled by a power of two to a
-  // largest magnitude in [2^14, 2^15): its 8 bits are kept exactly down to
-  // 2^-31 of that, and what is lost below is under fp32's own rounding.  The
-  // channels met by n 2^-20 are scaled by 2^-4 more.  A nibble is c + 8: each
-  // group's sum is short of -8 times its sum of q, and the logit of -8 sum_g
+  // largest magnitude in [2^14, 2^15), the channels met by n 2^-20 by 2^-4
+  // more: its 8 bits are kept exactly down to 2^-31 of that, or 2^-27.  The
+  // instruction keeps 25 bits below the exponents of the largest query and of
+  // 2^-14 (as in the second product, below), so a channel's product loses less
+  // than 2^-15 of the largest |q| of its group: with one channel 64 times the
+  // others the lse is off by 7e-5, at like magnitudes by 1e-6.  A nibble is c +
+  // 8: each group's sum is short of -8 times its sum of q, and the logit of -8 sum_g
   // ks_g sum q_g: one product of the scales with that sum in three bf16 parts
   // (24 bits), k slots 0..3 the high parts of groups 0..3, 4..7 the middle,
   // 8..11 the low ones.

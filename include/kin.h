@@ -404,11 +404,14 @@ kin_status kin_kv4_load(const kin_dims* dims, const kin_kv* kv, const int32_t* s
  * rounded to 11 (4 bit) or 16 (bf16) bits before they meet the values; over
  * 4-bit rows the smallest ones lose at most 2^-11 of sum p s in all (s a
  * token's scale), however far the tokens' weights are apart, and their scales
- * up to 2^80.  Sums are fp32.  NaN logits or values give NaN outputs.  Over
- * bf16 rows, values of any magnitude average without overflow (below 2^-80
- * they lose bits); over 4-bit rows, queries below 2^118 and values below 2^96
- * in magnitude are safe from it.  A length outside [1, Lcap] gets out = 0, lse = -inf and
- * flags KIN_ERR_DEVICE_DATA.
+ * up to 2^80.  Sums are fp32; a logit over 4-bit rows is off by at most
+ * 2^-10 softmax_scale sum_g s_g max |q_g| more (g: groups of 32 channels), and
+ * only where a channel's query is 2^-7 of its group's largest or less.  NaN
+ * logits or values give NaN outputs.  Over bf16 rows, values of any magnitude
+ * average without overflow (below 2^-80 they lose bits); over 4-bit rows,
+ * queries below 2^118 and values below 2^90 in magnitude are safe from it.  A
+ * length outside [1, Lcap] gets out = 0, lse = -inf and flags
+ * KIN_ERR_DEVICE_DATA.
  * workspace: kin_kv_attn_workspace_bytes for the same k_blocks (with_acc 1
  * where acc is given), 256-byte aligned and zero-filled before its first use
  * like kin_workspace_bytes'; with k_blocks >= 2 it serves the select calls
