@@ -22,7 +22,7 @@ import pytest
 import torch
 
 import block_top_sparse_kin_b200 as kin
-from test_gpu_kv import Cache, D, check_attention, gen, rows16, status
+from test_gpu_kv import Cache, D, check_attention, gen, random_selection, rows16, status
 
 pytestmark = pytest.mark.gpu
 
@@ -125,3 +125,29 @@ def test_bf16_values_at_the_ends_of_their_range(n, bs):
         out, lse = torch.full_like(q, 9.0), torch.empty((1, 8), device="cuda")
         kin.kin_kv_decode_attn(d, q, c.bf16(), c.seq, None, None, 0, 0.0, out, lse, ws)
         check_attention(c, q, out, lse, None, None, False)
+
+
+@pytest.mark.parametrize("k", [0, 40], ids=["every_block", "kept_blocks"])
+@pytest.mark.parametrize("g", [3, 8])
+def test_scales_far_apart_over_long_ranges(g, k):
+    """Warps of up to 64 tiles, ranges that are merged, ragged and paged
+    sequences: rows without a value, huge values under tiny weights and light
+    tokens beside heavy ones.  1024 tokens a warp: 1024 * 2^-24 * 2^3 = 2^-11
+    of sum p s from the small weights, 23 * 64 * 2^-23 < 2^-12 from the running
+    sums and 2^-15 from the tiles' products, less than 6 * 2^-13."""
+    c = Cache([20000, 4097, 1], 2, 32, 20010, True, 251)
+    u = pointed(c, list(range(50, 20000, 997)))[0, 0]
+    c.k[0, :, 7000], c.k[0, :, 12345] = 1.5 * u, 1.2 * u
+    c.v[0, :, 50::997] *= 2.0**40
+    c.v[0, :, 64::640], c.v[1, :, 100:200] = 0, 0
+    for b, n in enumerate(c.lens):
+        c.k[b, :, n:], c.v[b, :, n:] = float("nan"), float("nan")
+    q = (rows16(252, 3, 2 * g, D).float() * 0.1 + u.float() * torch.linspace(1, 0.2, 2 * g, device="cuda")[None, :, None]).to(torch.bfloat16)
+    sel, cnt = random_selection(c, k, 253) if k else (None, None)
+    dev = (sel.cuda(), cnt.cuda()) if k else (None, None)
+    d, st = c.dims(g), status()
+    out, lse, acc = torch.full_like(q, 9.0), torch.empty(q.shape[:2], device="cuda"), torch.zeros((3, 2, 20010), device="cuda")
+    kin.kin_kv_decode_attn(d, q, c.stored(), c.seq, *dev, k, 0.0, out, lse, kin.alloc_kv_attn_workspace(d, k, acc=True), acc=acc,
+                           dev_status=st)
+    assert int(st.item()) == 0
+    check_attention(c, q, out, lse, acc, None, True, sel.tolist() if k else None, tiles=192)
